@@ -542,6 +542,163 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
                                         float k_scale, float v_scale, int32_t partition_size,
                                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Scored paged attention: decode and multi-query attention for models whose
+ * scores are capped by a tanh or biased by distance, or whose query tokens see
+ * only a part of the context. The pages have no counterpart to these calls;
+ * they serve models with such layers over the same pool, block tables and
+ * slots as the calls above.
+ *
+ * Query token t of sequence s sits at position p (decode: its last position,
+ * context_lens[s] - 1; multi-query: as in paged_attention_multi_query). For
+ * query head h, kv head g and key position j:
+ *     x_j = scale * dot(query[t][h][:], K_j)
+ *     x_j = softcap * tanh(x_j / softcap)                if softcap > 0
+ *     x_j = x_j - alibi_slopes[h] * |p - j|              if alibi_slopes
+ *     out[t][h][:] = sum_j softmax(x)_j * V_j            over lo <= j < hi
+ *     lo = max(0, p - window + 1 if window > 0, key_begin[t] if key_begin)
+ *     hi = min(context_lens[s], key_end[t]) if key_end, else p + 1
+ * A token that sees no key (hi <= lo, or an empty context in decode) gives
+ * zeros. The intervals express the usual masks: a document mask is the first
+ * position of each token's document in key_begin; a prefix mask is key_end[t] =
+ * max(p + 1, prefix length); key_end[t] = context length everywhere is
+ * attention without a causal mask. Their values need not be sorted, and may
+ * lie outside the context (they are clamped to it).
+ *
+ *   softcap        finite and >= 0; 0 is no cap
+ *   alibi_slopes   [num_heads] fp32 device memory, or NULL
+ *   window         >= 0; 0 is no window. The token's own position counts
+ *   key_begin      [num_query_tokens] int32 (decode: [num_seqs]) device memory, or NULL
+ *   key_end        [num_query_tokens] int32 device memory, or NULL (multi-query)
+ *   workspace      paged_attention_scored_workspace_size(...) bytes, 16-byte
+ *                  aligned; may be NULL when that size is 0
+ *   *_fp8          over an E4M3 pool, k_scale and v_scale as in
+ *                  paged_attention_decode_fp8; head_dim 128 only
+ *
+ * Block-table entries whose tokens no query token of the sequence sees are not
+ * read, so that the blocks behind a window may have been given to others, and
+ * K and V rows outside a query token's interval never change its result,
+ * whatever they hold. A tanh, an exponential and every sum are computed in
+ * fp32; the softmax weights are rounded to the MMA's 16-bit type for their
+ * product with V. Every other argument, the dtypes, the error word and the
+ * treatment of bad inputs are those of paged_attention_decode and
+ * paged_attention_multi_query (a bad query_start_loc skips its sequence and
+ * sets PKV_DEVERR_QUERY; a bad block id skips its tokens and sets
+ * PKV_DEVERR_BLOCK_ID). Rows of out past the last sequence are not written.
+ */
+size_t paged_attention_scored_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t block_size, int32_t max_query_len,
+                                             int32_t max_context_len, int32_t window, int32_t partition_size);
+
+pkv_status_t paged_attention_decode_scored(void* out, const void* query, const void* key_cache,
+                                           const void* value_cache, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                                           int32_t max_context_len, float scale, float softcap,
+                                           const float* alibi_slopes, int32_t window, const int32_t* key_begin,
+                                           int32_t block_size, int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+                                           int32_t partition_size, void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
+pkv_status_t paged_attention_decode_scored_fp8(void* out, const void* query, const void* key_cache,
+                                               const void* value_cache, const int32_t* block_tables,
+                                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                               int32_t num_seqs, int32_t max_context_len, float scale, float softcap,
+                                               const float* alibi_slopes, int32_t window, const int32_t* key_begin,
+                                               int32_t block_size, int32_t num_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype, float k_scale,
+                                               float v_scale, int32_t partition_size, void* workspace,
+                                               size_t workspace_bytes, cudaStream_t stream);
+
+pkv_status_t paged_attention_multi_query_scored(
+    void* out, const void* query, const void* key_cache, const void* value_cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+    int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len, float scale, float softcap,
+    const float* alibi_slopes, int32_t window, const int32_t* key_begin, const int32_t* key_end, int32_t block_size,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+    int32_t partition_size, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+pkv_status_t paged_attention_multi_query_scored_fp8(
+    void* out, const void* query, const void* key_cache, const void* value_cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+    int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len, float scale, float softcap,
+    const float* alibi_slopes, int32_t window, const int32_t* key_begin, const int32_t* key_end, int32_t block_size,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype, float k_scale,
+    float v_scale, int32_t partition_size, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * paged_kv_reserve_slots -- block tables and slot map of the next step, built
+ * on the GPU from the request lengths: what the pages' append step does on the
+ * host ("Sparse Computation and Memory Management for Efficient LLM
+ * Inference", Memory Allocation Pseudocode; "KV Cache와 PagedAttention 완전
+ * 해부", §5단계: a block is handed out when the last one is full).
+ *
+ * Sequence s holds n = context_lens[s] tokens and gets k = new_lens[s] more.
+ * It needs ceil((n + k) / B) - ceil(n / B) new blocks, taken from the top of
+ * the free stack free_blocks[0 .. num_free[0] - 1]: the i-th block handed out
+ * by the call, in sequence and then position order, is free_blocks[num_free[0]
+ * - 1 - i]. A sequence is granted its tokens if it needs no block, or if the
+ * blocks it and all sequences before it need are in the stack (no sequence
+ * overtakes one that waits). For a granted sequence
+ *     block_tables[s][ceil(n / B) ...]   = its new blocks
+ *     slot_mapping[query_start_loc[s] + i] = slot of position n + i
+ *     context_lens_out[s] = n + k,  granted[s] = 1
+ * and for another one its slots are -1 (paged_kv_write skips them),
+ * context_lens_out[s] = n and granted[s] = 0. In both cases
+ *     query_start_loc[s] = new_lens[0] + ... + new_lens[s - 1]
+ *     num_free_out[0] = num_free[0] - blocks handed out
+ * and slot_mapping entries past the last token are -1.
+ *
+ *   block_tables     [num_seqs][max_blocks_per_seq] int32, updated in place
+ *   context_lens, new_lens, context_lens_out, granted   [num_seqs] int32
+ *   free_blocks      [free_capacity] int32;  num_free, num_free_out  [1] int32
+ *   slot_mapping     [max_tokens] int64;  query_start_loc  [num_seqs + 1] int32
+ * All in device memory. The *_out arrays and granted must not overlap the
+ * inputs (PKV_ERR_INVALID_ARG). The call reads its inputs only, apart from the
+ * new table entries, so that repeating it with the same inputs gives the same
+ * result. The blocks of a table are its sequence's alone: shared blocks
+ * (copy-on-write) are the host BlockPool's.
+ *
+ * Device-side checks: a negative length, or n + k > max_blocks_per_seq * B,
+ * refuses the sequence and sets PKV_DEVERR_CONTEXT; tokens past max_tokens
+ * refuse their sequence and set PKV_DEVERR_QUERY; num_free outside [0,
+ * free_capacity] is clamped and sets PKV_DEVERR_BLOCK_ID, as does a block id
+ * outside [0, num_blocks), whose slots are -1 (and a new one's table entry).
+ * block_size 8, 16 or 32; num_seqs <= 65535. One launch, asynchronous on
+ * `stream`; the pointers need no more than their type's alignment.
+ */
+pkv_status_t paged_kv_reserve_slots(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                    const int32_t* new_lens, const int32_t* free_blocks, int32_t free_capacity,
+                                    const int32_t* num_free, int64_t* slot_mapping, int32_t max_tokens,
+                                    int32_t* query_start_loc, int32_t* context_lens_out, int32_t* num_free_out,
+                                    int32_t* granted, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
+                                    cudaStream_t stream);
+
+/*
+ * paged_kv_release_blocks -- push the blocks of finished sequences back on the
+ * free stack of paged_kv_reserve_slots ("Sparse Computation and Memory
+ * Management for Efficient LLM Inference", Memory Allocation Pseudocode: a
+ * finished sequence's blocks return to the free list).
+ *
+ * For every s with finished[s] != 0, in order, its ceil(context_lens[s] / B)
+ * table entries are appended at free_blocks[num_free[0]] and on;
+ * context_lens_out[s] = 0. For the others context_lens_out[s] =
+ * context_lens[s]. num_free_out[0] = num_free[0] + blocks pushed. The tables
+ * keep their entries (a context of 0 says that they are stale).
+ *
+ * Shapes, overlap rule and limits as in paged_kv_reserve_slots; free_blocks is
+ * updated in place. Device-side checks: a context outside [0,
+ * max_blocks_per_seq * B] is clamped and sets PKV_DEVERR_CONTEXT; a table entry
+ * outside [0, num_blocks) is pushed as -1 and sets PKV_DEVERR_BLOCK_ID (a
+ * reserve refuses to hand it out); blocks past free_capacity are not written
+ * and set PKV_DEVERR_BLOCK_ID, num_free_out then being free_capacity.
+ */
+pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, const int32_t* finished, int32_t* free_blocks,
+                                     int32_t free_capacity, const int32_t* num_free, int32_t* context_lens_out,
+                                     int32_t* num_free_out, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
+                                     cudaStream_t stream);
+
 /* Static string naming a status code. */
 const char* pkv_status_string(pkv_status_t status);
 

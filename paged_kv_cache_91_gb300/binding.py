@@ -82,6 +82,21 @@ def load():
     lib.paged_attention_decode_fp8.restype = i32
     lib.paged_attention_decode_fp8.argtypes = [P, P, P, P, P, i32, P, i32, i32, f32, i32, i32, i32, i32, i32, i32,
                                                f32, f32, i32, P, sz, P]
+    lib.paged_attention_scored_workspace_size.restype = sz
+    lib.paged_attention_scored_workspace_size.argtypes = [i32] * 9
+    scored = [P, P, P, P, P, i32, P]          # out, query, caches, tables, table width, contexts
+    rules = [f32, f32, P, i32, P]             # scale, softcap, slopes, window, key_begin
+    shape = [i32, i32, i32, i32, i32, i32]    # block size, heads, kv heads, head dim, blocks, dtype
+    work = [i32, P, sz, P]                    # partition, workspace, its bytes, stream
+    for name, own in (("decode", [i32, i32] + rules), ("multi_query", [P, i32, i32, i32, i32] + rules + [P])):
+        for fp8 in ("", "_fp8"):
+            fn = getattr(lib, f"paged_attention_{name}_scored{fp8}")
+            fn.restype = i32
+            fn.argtypes = scored + own + shape + ([f32, f32] if fp8 else []) + work
+    lib.paged_kv_reserve_slots.restype = i32
+    lib.paged_kv_reserve_slots.argtypes = [P, i32, P, P, P, i32, P, P, i32, P, P, P, P, i32, i32, i32, P]
+    lib.paged_kv_release_blocks.restype = i32
+    lib.paged_kv_release_blocks.argtypes = [P, i32, P, P, P, i32, P, P, P, i32, i32, i32, P]
     _lib = lib
     return lib
 
@@ -438,6 +453,224 @@ def paged_attention_decode_shared_prefix_fp8(out: torch.Tensor, query: torch.Ten
     """paged_attention_decode_shared_prefix over an E4M3 pool (elements code * k_scale, code * v_scale)."""
     return _shared_prefix(out, query, key_cache, value_cache, prefix_blocks, prefix_len, block_tables, tail_lens,
                           scale, max_tail_len, workspace, stream, True, k_scale, v_scale)
+
+
+def paged_attention_scored_workspace_size(num_query_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                          block_size: int, max_query_len: int, max_context_len: int, window: int = 0,
+                                          partition_size: int = 0) -> int:
+    return int(load().paged_attention_scored_workspace_size(num_query_tokens, num_heads, num_kv_heads, head_dim,
+                                                            block_size, max_query_len, max_context_len, window,
+                                                            partition_size))
+
+
+def _launch(fn, device: torch.device, stream, *args) -> None:
+    """Call fn(*args, stream handle) with the tensors' device current (the library launches on the current one)."""
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        handle = _stream_of(device, stream)
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_of(device, stream))
+    if status != 0:
+        _check(load(), status)
+
+
+def _stream_of(device: torch.device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _same_device(first: torch.Tensor, **tensors) -> None:
+    for n, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise PagedKVError(-1, f"{n} is on {t.device}, query and tables on {first.device}")
+
+
+def _scored(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale, softcap,
+            alibi_slopes, window, key_begin, key_end, max_query_len, max_context_len, partition_size, workspace,
+            stream, fp8, k_scale, v_scale):
+    lib = load()
+    dt = _cuda16("query", query)
+    if _cuda16("out", out) != dt:
+        raise PagedKVError(-1, "out dtype differs from query")
+    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
+        if fp8:
+            _cuda_fp8(n, t)
+        elif _cuda16(n, t) != dt:
+            raise PagedKVError(-1, f"{n} dtype differs from query")
+    _cuda_i32("block_tables", block_tables)
+    _cuda_i32("context_lens", context_lens)
+    if key_cache.dim() != 4 or query.dim() != 3:
+        raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim] and query [rows][heads][head dim]")
+    NB, Hkv, B, D = key_cache.shape
+    T, H, D2 = query.shape
+    if D2 != D or out.shape != query.shape or value_cache.shape != key_cache.shape:
+        raise PagedKVError(-1, "shape mismatch between query, out and caches")
+    S = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1:
+        raise PagedKVError(-1, "block_tables must be [S][max_blocks] and context_lens [S]")
+    decode = query_start_loc is None
+    if decode:
+        if T != S:
+            raise PagedKVError(-1, f"query has {T} rows for {S} sequences")
+        max_query_len = 1
+    else:
+        _cuda_i32("query_start_loc", query_start_loc)
+        if query_start_loc.shape != (S + 1,):
+            raise PagedKVError(-1, "query_start_loc must be [S + 1]")
+        if max_query_len is None:
+            max_query_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_cuda
+                                     or not alibi_slopes.is_contiguous() or alibi_slopes.shape != (H,)):
+        raise PagedKVError(-1, "alibi_slopes must be a contiguous CUDA float32 tensor [num_heads]")
+    for n, t in (("key_begin", key_begin), ("key_end", key_end)):
+        if t is not None:
+            _cuda_i32(n, t)
+            if t.shape != (T,):
+                raise PagedKVError(-1, f"{n} must have one entry per query row")
+    _same_device(query, out=out, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
+                 context_lens=context_lens, query_start_loc=query_start_loc, alibi_slopes=alibi_slopes,
+                 key_begin=key_begin, key_end=key_end, workspace=workspace)
+    maxb = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = maxb * B
+    if workspace is None:
+        need = int(lib.paged_attention_scored_workspace_size(T, H, Hkv, D, B, int(max_query_len), int(max_context_len),
+                                                             int(window), int(partition_size)))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    head = (_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), maxb, _ptr(context_lens))
+    rules = (float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(key_begin))
+    shape = (B, H, Hkv, D, NB, dt) + ((float(k_scale), float(v_scale)) if fp8 else ())
+    work = (int(partition_size), _ptr(workspace), wbytes)
+    if decode:
+        fn = lib.paged_attention_decode_scored_fp8 if fp8 else lib.paged_attention_decode_scored
+        _launch(fn, query.device, stream, *head, S, int(max_context_len), *rules, *shape, *work)
+    else:
+        fn = lib.paged_attention_multi_query_scored_fp8 if fp8 else lib.paged_attention_multi_query_scored
+        _launch(fn, query.device, stream, *head, _ptr(query_start_loc), S, T, int(max_query_len),
+                int(max_context_len), *rules, _ptr(key_end), *shape, *work)
+    return out
+
+
+def paged_attention_decode_scored(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  scale: float, softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                                  window: int = 0, key_begin: Optional[torch.Tensor] = None,
+                                  max_context_len: Optional[int] = None, partition_size: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_decode with capped scores (``softcap`` > 0), a distance bias (``alibi_slopes`` [H] fp32), a
+    sliding ``window`` (0: none) and a first visible key per sequence (``key_begin`` [S] int32)."""
+    return _scored(out, query, key_cache, value_cache, block_tables, context_lens, None, scale, softcap,
+                   alibi_slopes, window, key_begin, None, 1, max_context_len, partition_size, workspace, stream,
+                   False, 1.0, 1.0)
+
+
+def paged_attention_decode_scored_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                      value_cache: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, scale: float, k_scale: float, v_scale: float,
+                                      softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                                      window: int = 0, key_begin: Optional[torch.Tensor] = None,
+                                      max_context_len: Optional[int] = None, partition_size: int = 0,
+                                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_decode_scored over an E4M3 pool (elements code * k_scale, code * v_scale); head_dim 128."""
+    return _scored(out, query, key_cache, value_cache, block_tables, context_lens, None, scale, softcap,
+                   alibi_slopes, window, key_begin, None, 1, max_context_len, partition_size, workspace, stream,
+                   True, k_scale, v_scale)
+
+
+def paged_attention_multi_query_scored(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                       value_cache: torch.Tensor, block_tables: torch.Tensor,
+                                       context_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                                       softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                                       window: int = 0, key_begin: Optional[torch.Tensor] = None,
+                                       key_end: Optional[torch.Tensor] = None, max_query_len: Optional[int] = None,
+                                       max_context_len: Optional[int] = None, partition_size: int = 0,
+                                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_multi_query with the scores of paged_attention_decode_scored; query token t sees the keys
+    [key_begin[t], key_end[t]) (int32 [T]; default: from 0, to its own position), cut by the window and the context.
+
+    ``max_query_len`` bounds every query length on the host; when omitted it is read from query_start_loc, which
+    synchronises the stream.
+    """
+    return _scored(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale, softcap,
+                   alibi_slopes, window, key_begin, key_end, max_query_len, max_context_len, partition_size,
+                   workspace, stream, False, 1.0, 1.0)
+
+
+def paged_attention_multi_query_scored_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                           value_cache: torch.Tensor, block_tables: torch.Tensor,
+                                           context_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                                           k_scale: float, v_scale: float, softcap: float = 0.0,
+                                           alibi_slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                           key_begin: Optional[torch.Tensor] = None,
+                                           key_end: Optional[torch.Tensor] = None,
+                                           max_query_len: Optional[int] = None,
+                                           max_context_len: Optional[int] = None, partition_size: int = 0,
+                                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_multi_query_scored over an E4M3 pool (elements code * k_scale, code * v_scale); head_dim 128."""
+    return _scored(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale, softcap,
+                   alibi_slopes, window, key_begin, key_end, max_query_len, max_context_len, partition_size,
+                   workspace, stream, True, k_scale, v_scale)
+
+
+def _pool_arrays(block_tables, context_lens, lens_name, lens, free_blocks, num_free, **outs) -> int:
+    """Check the arrays that the reserve and release calls share; returns the number of sequences."""
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), (lens_name, lens),
+                 ("free_blocks", free_blocks), ("num_free", num_free), *outs.items()):
+        _cuda_i32(n, t)
+    S = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1 or lens.shape != (S,):
+        raise PagedKVError(-1, f"block_tables must be [S][max_blocks], context_lens and {lens_name} [S]")
+    if free_blocks.dim() != 1 or num_free.numel() != 1 or outs["num_free_out"].numel() != 1:
+        raise PagedKVError(-1, "free_blocks must be a vector, num_free and num_free_out one element")
+    for n, t in outs.items():
+        want = S + 1 if n == "query_start_loc" else 1 if n == "num_free_out" else S
+        if t.numel() != want:
+            raise PagedKVError(-1, f"{n} must have {want} elements")
+    _same_device(block_tables, context_lens=context_lens, free_blocks=free_blocks, num_free=num_free,
+                 **{lens_name: lens}, **outs)
+    return S
+
+
+def paged_kv_reserve_slots(block_tables: torch.Tensor, context_lens: torch.Tensor, new_lens: torch.Tensor,
+                           free_blocks: torch.Tensor, num_free: torch.Tensor, slot_mapping: torch.Tensor,
+                           query_start_loc: torch.Tensor, context_lens_out: torch.Tensor,
+                           num_free_out: torch.Tensor, granted: torch.Tensor, block_size: int, num_blocks: int,
+                           stream=None) -> None:
+    """Slots for new_lens[s] more tokens of each sequence, with blocks from the top of the free stack
+    free_blocks[:num_free]: updates block_tables in place and writes slot_mapping [max_tokens] int64 (-1: padding,
+    or a sequence that got nothing), query_start_loc [S + 1], context_lens_out [S], num_free_out [1] and granted [S].
+    The outputs must not overlap the inputs."""
+    lib = load()
+    S = _pool_arrays(block_tables, context_lens, "new_lens", new_lens, free_blocks, num_free,
+                     query_start_loc=query_start_loc, context_lens_out=context_lens_out, num_free_out=num_free_out,
+                     granted=granted)
+    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_cuda or not slot_mapping.is_contiguous():
+        raise PagedKVError(-1, "slot_mapping must be a contiguous CUDA int64 tensor")
+    _same_device(block_tables, slot_mapping=slot_mapping)
+    _launch(lib.paged_kv_reserve_slots, block_tables.device, stream, _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), _ptr(new_lens), _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
+            _ptr(slot_mapping), slot_mapping.numel(), _ptr(query_start_loc), _ptr(context_lens_out),
+            _ptr(num_free_out), _ptr(granted), S, int(block_size), int(num_blocks))
+
+
+def paged_kv_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, finished: torch.Tensor,
+                            free_blocks: torch.Tensor, num_free: torch.Tensor, context_lens_out: torch.Tensor,
+                            num_free_out: torch.Tensor, block_size: int, num_blocks: int, stream=None) -> None:
+    """Push the blocks of the sequences with finished[s] != 0 on the free stack free_blocks (in place), and write
+    context_lens_out [S] (0 for them) and num_free_out [1]. The outputs must not overlap the inputs."""
+    lib = load()
+    S = _pool_arrays(block_tables, context_lens, "finished", finished, free_blocks, num_free,
+                     context_lens_out=context_lens_out, num_free_out=num_free_out)
+    _launch(lib.paged_kv_release_blocks, block_tables.device, stream, _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), _ptr(finished), _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
+            _ptr(context_lens_out), _ptr(num_free_out), S, int(block_size), int(num_blocks))
 
 
 def device_errors(clear: bool = True) -> int:

@@ -54,6 +54,8 @@ constexpr int kMaxDevices = 64;
 
 thread_local char g_msg[512] = "";
 
+}  // namespace
+
 pkv_status_t fail(pkv_status_t st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -65,6 +67,8 @@ pkv_status_t fail(pkv_status_t st, const char* fmt, ...) {
 pkv_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "paged_kv.h"
+
 namespace pkv {
 
 struct DecodeParams;
@@ -63,6 +65,9 @@ cudaError_t decode_mq_pairs_fp8_bf16(const DecodeParams& p, const MqParams& mq, 
 
 // Set the calling thread's pkv_last_error_message() text.
 void set_last_error_message(const char* msg);
+// The same from a format, returning the status (cuda_fail: PKV_ERR_CUDA with the CUDA error's text).
+pkv_status_t fail(pkv_status_t st, const char* fmt, ...);
+pkv_status_t cuda_fail(cudaError_t e, const char* what);
 
 // The device address of a device's error word (PKV_DEVERR_* bits), or null.
 unsigned* device_error_word(int dev);

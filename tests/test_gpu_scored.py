@@ -1,0 +1,305 @@
+"""Scored paged attention (tanh cap, distance bias, window, key intervals) on the GPU against the definition in
+64 bits, within the error that the formats allow (tests/scored_reference.py)."""
+import pytest
+import torch
+
+import scored_reference as R
+from paged_kv_cache_91_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word(cuda_lib):
+    binding.device_errors(clear=True)
+    yield
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def call(b, softcap=0.0, slopes=None, window=0, key_begin=None, key_end=None, out=None, max_ctx=None, **kw):
+    out = torch.full_like(b["q"], float("nan"), device=DEV) if out is None else out
+    args = [out, b["q"].to(DEV), b["kc"].to(DEV), b["vc"].to(DEV), b["tables"].to(DEV), i32(b["ctx"])]
+    kw = dict(kw, softcap=softcap, window=window, alibi_slopes=None if slopes is None else slopes.to(DEV),
+              key_begin=None if key_begin is None else i32(key_begin),
+              max_context_len=max(b["ctx"]) if max_ctx is None else max_ctx)
+    if b["fp8"]:
+        kw.update(k_scale=b["k_scale"], v_scale=b["v_scale"])
+    if b["decode"]:
+        fn = binding.paged_attention_decode_scored_fp8 if b["fp8"] else binding.paged_attention_decode_scored
+        fn(*args, b["scale"], **kw)
+    else:
+        fn = binding.paged_attention_multi_query_scored_fp8 if b["fp8"] else binding.paged_attention_multi_query_scored
+        kw.setdefault("max_query_len", max(b["qlens"]))
+        fn(*args, i32(b["starts"]), b["scale"], key_end=None if key_end is None else i32(key_end), **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(b, errors=0, part=0, **rules):
+    ref, tol = R.reference(b, **rules)
+    out = call(b, partition_size=part, **rules)
+    assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == errors
+
+
+DECODE_CTX = [0, 1, 7, 8, 9, 31, 33, 64, 65, 200, 300, 511, 777]
+SHAPES = [  # H, Hkv, D, B, dtype, fp8
+    (4, 4, 64, 16, "f16", False), (8, 2, 128, 16, "bf16", False), (6, 2, 64, 8, "bf16", False),
+    (8, 8, 128, 32, "f16", False), (16, 1, 128, 8, "f16", False), (20, 4, 128, 16, "bf16", False),
+    (8, 1, 128, 16, "bf16", True), (4, 4, 128, 8, "f16", True), (24, 2, 128, 32, "bf16", True),
+]
+RULES = ["none", "cap", "alibi", "window", "begin", "all"]
+
+
+def rules_of(name, b, seed=5):
+    r = {}
+    if name in ("cap", "all"):
+        r["softcap"] = 3.0  # the scores' spread is about 2: both sides of the tanh's bend
+    if name in ("alibi", "all"):
+        r["slopes"] = R.slopes_of(b["H"])
+    if name in ("window", "all"):
+        r["window"] = 70
+    if name in ("begin", "all"):
+        r["key_begin"] = R.documents(b, seed)
+    return r
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", SHAPES)
+def test_decode(H, Hkv, D, B, dtype, fp8, rule):
+    b = R.build(11, DECODE_CTX, None, H, Hkv, D, B, dtype, fp8)
+    check(b, **rules_of(rule, b))
+
+
+@pytest.mark.parametrize("rule", ["cap", "window", "all"])
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", [SHAPES[1], SHAPES[3], SHAPES[5], SHAPES[6]])
+def test_decode_split(H, Hkv, D, B, dtype, fp8, rule):
+    """Contexts of several partitions (64 tokens each), and a context length bound above them all."""
+    b = R.build(12, [1, 64, 65, 129, 640, 901], None, H, Hkv, D, B, dtype, fp8)
+    check(b, part=64, **rules_of(rule, b))
+    ref, tol = R.reference(b, **rules_of(rule, b))
+    out = call(b, partition_size=64, max_ctx=b["tables"].shape[1] * B, **rules_of(rule, b))
+    assert R.worst(out, ref, tol) <= 1.0
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 1 << 30])
+def test_decode_windows(window):
+    b = R.build(13, [1, 2, 15, 16, 17, 100, 500], None, 8, 2, 128, 16)
+    check(b, window=window)
+
+
+@pytest.mark.parametrize("softcap", [1e-3, 0.5, 50.0, 1e6])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_decode_caps(softcap, dtype):
+    """Far into the cap, and caps that no score comes near."""
+    b = R.build(14, [3, 90, 400], None, 8, 2, 128, 16, dtype, spread=4.0)
+    check(b, softcap=softcap)
+
+
+MQ = [  # contexts, query lengths
+    ([5, 40, 131, 300], [5, 4, 131, 64]),       # whole prompts and chunks
+    ([1, 77, 200, 64, 9], [1, 0, 3, 64, 2]),    # one token, none, few
+    ([700], [150]),
+]
+MQ_RULES = ["none", "cap", "alibi", "window", "documents", "prefix", "full", "all"]
+
+
+def mq_rules(name, b):
+    r = {}
+    if name in ("cap", "all"):
+        r["softcap"] = 3.0
+    if name in ("alibi", "all"):
+        r["slopes"] = R.slopes_of(b["H"])
+    if name in ("window", "all"):
+        r["window"] = 50
+    if name == "documents":
+        r["key_begin"] = R.documents(b, 8)
+    if name in ("prefix", "all"):
+        r["key_end"] = R.prefixes(b, 9)
+    if name == "full":  # no causal mask, distances on both sides
+        r["key_end"] = [1 << 30] * b["q"].shape[0]
+        r["slopes"] = R.slopes_of(b["H"])
+    return r
+
+
+@pytest.mark.parametrize("rule", MQ_RULES)
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", SHAPES)
+def test_multi_query(H, Hkv, D, B, dtype, fp8, rule):
+    for ctx, qlens in MQ[:2]:
+        b = R.build(21, ctx, qlens, H, Hkv, D, B, dtype, fp8)
+        check(b, **mq_rules(rule, b))
+
+
+@pytest.mark.parametrize("rule", ["cap", "window", "documents", "prefix", "all"])
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", [SHAPES[0], SHAPES[1], SHAPES[5], SHAPES[6]])
+def test_multi_query_split(H, Hkv, D, B, dtype, fp8, rule):
+    b = R.build(22, *MQ[2], H, Hkv, D, B, dtype, fp8)
+    check(b, part=128, **mq_rules(rule, b))
+
+
+@pytest.mark.parametrize("q", [1, 3, 40])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_that_see_nothing(q, fp8):
+    """Empty intervals, among rows that see something and all through a sequence, give zeros; values far
+    outside the context are clamped."""
+    b = R.build(23, [60, 200], [q, q], 8, 2, 128, 16, fp8=fp8)
+    T = 2 * q
+    begin = [(1 << 31) - 1 if t % 3 == 0 else -(1 << 31) for t in range(T)]
+    end = [(1 << 31) - 1 if t % 2 else 30 for t in range(T)]
+    check(b, key_begin=begin, key_end=end, softcap=2.0)
+    check(b, key_begin=[0] * T, key_end=[-(1 << 31)] * T)
+    check(b, key_begin=[100] * T, key_end=[100] * T, window=5, slopes=R.slopes_of(8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_decode_masked_keys_may_hold_anything(what, fp8):
+    if fp8 and what == "inf":
+        pytest.skip("E4M3 has no infinity")
+    b = R.build(24, [40, 300, 90], None, 8, 2, 128, 16, fp8=fp8)
+    begin = [3, 250, 89]
+    bad = 0x7F if fp8 else float(what)
+    for s, lo in enumerate(begin):
+        for j in range(lo):
+            for pool in (b["kc"], b["vc"]):
+                pool[b["tables"][s, j // 16], :, j % 16] = bad
+    check(b, key_begin=begin, softcap=5.0)
+    check(b, key_begin=begin, slopes=R.slopes_of(8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("qlens", [[2, 3], [60, 90]])
+@pytest.mark.parametrize("part", [0, 64])
+def test_a_key_of_others_never_reaches_a_row(qlens, fp8, part):
+    """NaN and infinities in keys that some rows see do not reach the rows that do not see them."""
+    b = R.build(25, [100, 200], qlens, 4, 2, 128, 16, "bf16", fp8)
+    T = sum(qlens)
+    rows = {}
+    for s, at in ((0, 97), (1, 150)):  # two keys of NaN values; the second sequence's rows all see past it
+        for pool in (b["kc"], b["vc"]):
+            pool[b["tables"][s, at // 16], :, at % 16] = 0x7F if fp8 else float("nan")
+        rows[s] = at
+    if not fp8:
+        b["vc"][b["tables"][1, 10], :, 3] = float("inf")
+    begin, end = [], []
+    for s, (n, ql) in enumerate(zip(b["ctx"], b["qlens"])):
+        for i in range(ql):
+            sees = i % 2 == 1
+            begin.append(0 if sees else rows[s] + 1 if s else 0)
+            end.append(n if sees else n if s else rows[s])
+    ref, tol = R.reference(b, key_begin=begin, key_end=end, softcap=4.0)
+    out = call(b, key_begin=begin, key_end=end, softcap=4.0, partition_size=part).double().cpu()
+    clean = [t for t in range(T) if torch.isfinite(ref[t]).all()]
+    assert clean and len(clean) < T
+    assert R.worst(out[clean], ref[clean], tol[clean]) <= 1.0
+    for t in range(T):
+        if t not in clean:
+            assert not torch.isfinite(out[t]).all()
+
+
+@pytest.mark.parametrize("qlens", [None, [4, 2], [70, 40]])
+def test_blocks_behind_the_window_are_not_read(qlens):
+    """Their table entries may be anything: no error is reported."""
+    b = R.build(26, [300, 150], qlens, 8, 2, 128, 16)
+    ref, tol = R.reference(b, window=20)
+    for s, (n, ql) in enumerate(zip(b["ctx"], b["qlens"])):
+        b["tables"][s, :(n - ql - 20 + 1) // 16] = -9 if s else 1 << 30
+    out = call(b, window=20)
+    assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("qlens", [None, [5, 3], [60, 90]])
+def test_bad_block_ids_are_skipped_and_reported(qlens):
+    b = R.build(27, [100, 200], qlens, 8, 2, 128, 16, fp8=False)
+    b["tables"][0, 1] = b["kc"].shape[0]
+    b["tables"][1, 4] = -1
+    check(b, errors=1, softcap=4.0, slopes=R.slopes_of(8))
+
+
+def test_contexts_are_clamped_and_reported():
+    b = R.build(28, [40, 90], None, 4, 2, 64, 16)
+    bad = dict(b, ctx=[-3, 400])
+    out = call(bad, max_ctx=90, softcap=5.0)
+    ref, tol = R.reference(b, softcap=5.0)
+    assert R.worst(out[1:], ref[1:], tol[1:]) <= 1.0
+    assert (out[0] == 0).all()
+    assert binding.device_errors() == 2
+
+
+@pytest.mark.parametrize("q", [3, 50])
+def test_bad_query_offsets_skip_their_sequence(q):
+    b = R.build(29, [60, 70, 80], [q, q, q], 8, 2, 128, 16)
+    ref, tol = R.reference(b, softcap=5.0)
+    for starts, good in (([0, q, q - 1, 3 * q], [0]), ([0, q, 2 * q, 3 * q + 1], [0, 1]), ([-1, q, 2 * q, 3 * q], [1, 2])):
+        # ([0, q, q - 1, 3q]: sequence 1 has a negative length, sequence 2 more tokens than max_query_len)
+        out = call(dict(b, starts=starts), softcap=5.0)
+        for s in range(3):
+            rows = slice(s * q, (s + 1) * q)
+            if s in good:
+                assert R.worst(out[rows], ref[rows], tol[rows]) <= 1.0
+            else:
+                assert torch.isnan(out[rows]).all()
+        assert binding.device_errors() == 16
+
+
+def test_rows_past_the_last_sequence_are_left_as_they_were():
+    b = R.build(30, [50, 90], [20, 30], 8, 2, 128, 16)
+    ref, tol = R.reference(b, window=33)
+    big = dict(b, q=torch.cat([b["q"], b["q"][:7]]))
+    out = torch.full_like(big["q"], 7.5, device=DEV)
+    call(big, window=33, out=out)
+    assert R.worst(out[:50], ref, tol) <= 1.0
+    assert (out[50:] == 7.5).all()
+
+
+@pytest.mark.parametrize("qlens", [None, [4, 9], [80, 33]])
+def test_other_stream_and_graph(qlens):
+    """On another stream, and captured once and replayed over new inputs."""
+    rules = dict(softcap=4.0, window=60, slopes=R.slopes_of(8))
+    one, two = (R.build(seed, [200, 170], qlens, 8, 2, 128, 16) for seed in (31, 32))
+    want = [R.reference(x, **rules) for x in (one, two)]
+    st = {k: one[k].to(DEV) for k in ("q", "kc", "vc", "tables")}
+    out = torch.empty_like(st["q"])
+    ctx, starts, slopes = i32(one["ctx"]), i32(one["starts"]), rules["slopes"].to(DEV)
+    mql = max(one["qlens"])
+    need = binding.paged_attention_scored_workspace_size(st["q"].shape[0], 8, 2, 128, 16, mql, 200, 60, 64)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+
+    def step(stream=None):
+        a = (out, st["q"], st["kc"], st["vc"], st["tables"], ctx)
+        kw = dict(softcap=4.0, window=60, alibi_slopes=slopes, max_context_len=200, partition_size=64, workspace=ws,
+                  stream=stream)
+        if qlens is None:
+            binding.paged_attention_decode_scored(*a, one["scale"], **kw)
+        else:
+            binding.paged_attention_multi_query_scored(*a, starts, one["scale"], max_query_len=mql, **kw)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    torch.cuda.synchronize()
+    assert R.worst(out, *want[0]) <= 1.0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in ("q", "kc", "vc", "tables"):
+        st[k].copy_(two[k])
+    for _ in range(2):
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert R.worst(out, *want[1]) <= 1.0
+
+
+@pytest.mark.parametrize("qlens", [None, [70, 90]])
+def test_same_inputs_give_the_same_bits(qlens):
+    b = R.build(33, [333, 500], qlens, 8, 2, 128, 16)
+    first = call(b, softcap=9.0, partition_size=64)
+    for _ in range(3):
+        assert torch.equal(call(b, softcap=9.0, partition_size=64), first)

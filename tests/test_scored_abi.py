@@ -1,0 +1,157 @@
+"""Scored attention and the block-table calls without a GPU: every refusal is made on the host."""
+import ctypes
+
+import pytest
+import torch
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_kv_cache_91_gb300 import binding
+    from paged_kv_cache_91_gb300 import build as b
+
+    b.build()
+    return binding.load()
+
+
+def fake(n):
+    """A non-null, aligned address that is never dereferenced on the host path."""
+    return P(0x10000 * n)
+
+
+def decode(lib, fp8=False, **kw):
+    a = dict(out=fake(1), query=fake(2), key_cache=fake(3), value_cache=fake(4), block_tables=fake(5),
+             max_blocks_per_seq=8, context_lens=fake(6), num_seqs=2, max_context_len=128, scale=0.125, softcap=0.0,
+             alibi_slopes=None, window=0, key_begin=None, block_size=16, num_heads=4, num_kv_heads=4, head_dim=128,
+             num_blocks=16, dtype=0)
+    if fp8:
+        a.update(k_scale=0.5, v_scale=0.25)
+    a.update(partition_size=0, workspace=None, workspace_bytes=0, stream=None)
+    a.update(kw)
+    fn = lib.paged_attention_decode_scored_fp8 if fp8 else lib.paged_attention_decode_scored
+    return fn(*a.values())
+
+
+def multi_query(lib, fp8=False, **kw):
+    a = dict(out=fake(1), query=fake(2), key_cache=fake(3), value_cache=fake(4), block_tables=fake(5),
+             max_blocks_per_seq=8, context_lens=fake(6), query_start_loc=fake(7), num_seqs=2, num_query_tokens=5,
+             max_query_len=4, max_context_len=128, scale=0.125, softcap=0.0, alibi_slopes=None, window=0,
+             key_begin=None, key_end=None, block_size=16, num_heads=4, num_kv_heads=4, head_dim=128, num_blocks=16,
+             dtype=0)
+    if fp8:
+        a.update(k_scale=0.5, v_scale=0.25)
+    a.update(partition_size=0, workspace=None, workspace_bytes=0, stream=None)
+    a.update(kw)
+    fn = lib.paged_attention_multi_query_scored_fp8 if fp8 else lib.paged_attention_multi_query_scored
+    return fn(*a.values())
+
+
+COMMON = [
+    (dict(softcap=-1.0), INVALID), (dict(softcap=float("nan")), INVALID), (dict(softcap=float("inf")), INVALID),
+    (dict(softcap=1e-45, scale=1e30), INVALID),  # scale / softcap overflows
+    (dict(window=-1), INVALID), (dict(scale=float("inf")), INVALID), (dict(num_heads=6), INVALID),
+    (dict(num_kv_heads=0), INVALID), (dict(head_dim=96), UNSUPPORTED), (dict(block_size=64), UNSUPPORTED),
+    (dict(dtype=2), INVALID), (dict(num_blocks=0), INVALID), (dict(max_blocks_per_seq=0), INVALID),
+    (dict(max_context_len=-1), INVALID), (dict(max_context_len=129), INVALID), (dict(out=None), INVALID),
+    (dict(context_lens=None), INVALID), (dict(query=P(0x20008)), INVALID), (dict(value_cache=P(0x40008)), INVALID),
+    (dict(num_seqs=-1), INVALID), (dict(num_seqs=70000), UNSUPPORTED), (dict(num_blocks=1 << 25), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw,status", COMMON)
+def test_decode_rejects_on_host(lib, kw, status, fp8):
+    assert decode(lib, fp8, **kw) == status
+    assert lib.pkv_last_error_message() != b""
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(query_start_loc=None), INVALID), (dict(num_query_tokens=-1), INVALID), (dict(max_query_len=-3), INVALID),
+    (dict(max_query_len=129), INVALID), (dict(num_query_tokens=1 << 30), UNSUPPORTED),
+])
+def test_multi_query_rejects_on_host(lib, kw, status, fp8):
+    assert multi_query(lib, fp8, **kw) == status
+    assert lib.pkv_last_error_message() != b""
+
+
+@pytest.mark.parametrize("call", [decode, multi_query])
+@pytest.mark.parametrize("kw,status", [
+    (dict(head_dim=64), UNSUPPORTED), (dict(k_scale=0.0), INVALID), (dict(v_scale=-1.0), INVALID),
+    (dict(k_scale=float("inf")), INVALID), (dict(v_scale=float("nan")), INVALID),
+])
+def test_fp8_rejects_on_host(lib, call, kw, status):
+    assert call(lib, True, **kw) == status
+
+
+def test_nothing_to_do_is_a_noop(lib):
+    for fp8 in (False, True):
+        assert decode(lib, fp8, num_seqs=0, out=None) == OK
+        assert multi_query(lib, fp8, num_seqs=0, out=None) == OK
+        assert multi_query(lib, fp8, num_query_tokens=0, out=None) == OK
+        assert multi_query(lib, fp8, max_query_len=0, out=None) == OK
+
+
+def reserve(lib, **kw):
+    a = dict(block_tables=fake(1), max_blocks_per_seq=8, context_lens=fake(2), new_lens=fake(3), free_blocks=fake(4),
+             free_capacity=4, num_free=fake(5), slot_mapping=fake(6), max_tokens=9, query_start_loc=fake(7),
+             context_lens_out=fake(8), num_free_out=fake(9), granted=fake(10), num_seqs=3, block_size=16,
+             num_blocks=8, stream=None)
+    a.update(kw)
+    return lib.paged_kv_reserve_slots(*a.values())
+
+
+def release(lib, **kw):
+    a = dict(block_tables=fake(1), max_blocks_per_seq=8, context_lens=fake(2), finished=fake(3), free_blocks=fake(4),
+             free_capacity=4, num_free=fake(5), context_lens_out=fake(8), num_free_out=fake(9), num_seqs=3,
+             block_size=16, num_blocks=8, stream=None)
+    a.update(kw)
+    return lib.paged_kv_release_blocks(*a.values())
+
+
+SLOTS = [
+    (dict(num_seqs=-1), INVALID), (dict(num_seqs=70000), UNSUPPORTED), (dict(block_size=12), UNSUPPORTED),
+    (dict(num_blocks=0), INVALID), (dict(max_blocks_per_seq=0), INVALID), (dict(free_capacity=-1), INVALID),
+    (dict(max_blocks_per_seq=1 << 27), UNSUPPORTED), (dict(block_tables=None), INVALID),
+    (dict(num_free=None), INVALID), (dict(num_free_out=None), INVALID), (dict(free_blocks=None), INVALID),
+    (dict(context_lens_out=None), INVALID), (dict(context_lens_out=fake(2)), INVALID),
+    (dict(context_lens_out=P(0x20008)), INVALID), (dict(num_free_out=fake(5)), INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,status", SLOTS + [
+    (dict(max_tokens=-1), INVALID), (dict(slot_mapping=None), INVALID), (dict(query_start_loc=None), INVALID),
+    (dict(granted=None), INVALID), (dict(granted=fake(2)), INVALID), (dict(granted=P(0x30004)), INVALID),
+    (dict(new_lens=None), INVALID),
+])
+def test_reserve_rejects_on_host(lib, kw, status):
+    assert reserve(lib, **kw) == status
+    assert lib.pkv_last_error_message() != b""
+
+
+@pytest.mark.parametrize("kw,status", SLOTS + [(dict(finished=None), INVALID), (dict(context_lens_out=fake(3)), INVALID)])
+def test_release_rejects_on_host(lib, kw, status):
+    assert release(lib, **kw) == status
+    assert lib.pkv_last_error_message() != b""
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    from paged_kv_cache_91_gb300 import binding
+
+    x = torch.zeros(2, 4, 64, dtype=torch.float16)
+    kc = torch.zeros(4, 4, 16, 64, dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    one = torch.zeros(1, dtype=torch.int32)
+    t = torch.zeros(2, 1, dtype=torch.int32)
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_attention_decode_scored(x, x, kc, kc, t, i, 0.125, softcap=5.0)
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_attention_multi_query_scored(x, x, kc, kc, t, i, torch.zeros(3, dtype=torch.int32), 0.125)
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_kv_reserve_slots(t, i, i, i, one, torch.zeros(4, dtype=torch.int64),
+                                       torch.zeros(3, dtype=torch.int32), i.clone(), one.clone(), i.clone(), 16, 4)
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_kv_release_blocks(t, i, i, i, one, i.clone(), one.clone(), 16, 4)
