@@ -9,6 +9,7 @@
 namespace pkv {
 
 struct DecodeParams;
+struct ScoreParams;
 
 // CUDA-core decode (any group size; one CTA per query head).
 cudaError_t decode_simt_f16(const DecodeParams& p, int head_dim, int block_size, int num_seqs,
@@ -62,6 +63,24 @@ cudaError_t decode_mq_pairs_fp8_f16(const DecodeParams& p, const MqParams& mq, c
 cudaError_t decode_mq_pairs_fp8_bf16(const DecodeParams& p, const MqParams& mq, const CUtensorMap& kmap,
                                      const CUtensorMap& vmap, int head_dim, int block_size, int num_seqs,
                                      cudaStream_t stream);
+
+// Scored attention (pkv_scored.cuh) on the 8-column tile; the pool through make_pool_map, or make_pool_map_tc
+// for a 16-bit pool of head_dim 128 (tile_one_copy()). f16: the query's and output's type (else bf16).
+cudaError_t scored_cols_16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                           const CUtensorMap& vmap, bool f16, int head_dim, int block_size, int num_seqs,
+                           cudaStream_t stream);
+cudaError_t scored_cols_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
+
+// Tensor maps of the pool (cuTensorMapEncodeTiled); false if the driver refuses.
+bool make_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int block_size,
+                   pkv_dtype_t dtype);
+bool make_pool_map_fp8_rows(CUtensorMap* map, const void* base, long long rows, int block_size);
+bool make_pool_map_tc(CUtensorMap* map, const void* base, long long rows, int block_size, pkv_dtype_t dtype);
+
+// The sequences by context length, longest first, into order[num_seqs].
+cudaError_t launch_mq_order(const int32_t* context_lens, int num_seqs, int ctx_limit, int32_t* order,
+                            cudaStream_t stream);
 
 // Set the calling thread's pkv_last_error_message() text.
 void set_last_error_message(const char* msg);

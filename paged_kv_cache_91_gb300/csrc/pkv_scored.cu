@@ -1,77 +1,81 @@
-// Scored paged attention: the entry points (argument checks, dispatch) and the kernel.
+// Scored paged attention: the entry points (argument checks, the plan of a call, dispatch) and the reduce kernel.
 #include <math.h>
 #include <stdint.h>
-
-#include <type_traits>
+#include <string.h>
 
 #include "paged_kv.h"
 #include "pkv_internal.h"
+#include "pkv_reduce.cuh"
 #include "pkv_scored.cuh"
 
 namespace pkv {
 namespace {
 
-// One warp per (query token, head): it walks the visible keys in order, its lanes holding D / 32 dims each,
-// with a running maximum and sum. C: the cache's element type.
-template <int D, typename C>
-__device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned char* row, int lane) {
-  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB;
-#pragma unroll
-  for (int e = 0; e < DPL / 2; ++e) {
-    const unsigned char* at = row + (lane * DPL + 2 * e) * EB;
-    const float2 f = CacheFmt<C>::pair(EB == 1 ? *reinterpret_cast<const uint16_t*>(at)
-                                               : *reinterpret_cast<const uint32_t*>(at));
-    v[2 * e] = f.x;
-    v[2 * e + 1] = f.y;
+// Merge of the partials of rows that span several partitions: a CTA takes 4 heads (a warp each) of
+// kReduceTokens query tokens of a sequence. Each row's first and last partition follow from its interval.
+constexpr int kReduceTokens = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kReduceRows)
+    pkv_scored_reduce_kernel(const DecodeParams p, const ScoreParams sc, int block_size) {
+  pdl_begin();
+  const int s = blockIdx.x, h = blockIdx.y * kReduceRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (h >= p.num_heads) return;
+  const int c = p.context_lens[s];
+  const int ctx = c < 0 ? 0 : (c > p.ctx_limit ? p.ctx_limit : c);
+  int q0 = 0;
+  const int q_len = scored_query_len(sc, s, ctx, q0);
+  const int base = scored_base(sc, ctx, q_len, block_size);
+  for (int i = blockIdx.z * kReduceTokens; i < min(q_len, (int)(blockIdx.z + 1) * kReduceTokens); ++i) {
+    int lo, hi;
+    scored_span(sc, q0 + i, ctx - q_len + i, ctx, lo, hi);
+    const RowParts parts = row_parts(lo, hi, base, p.partition_size);
+    if (parts.direct()) continue;  // written by the attention kernel
+    const size_t row = (size_t)(q0 + i) * p.num_heads + h;
+    const size_t at = row * p.max_partitions + parts.first;
+    float mp, lp;
+    float o_early[kReduceEarly][D / 32];
+    reduce_load_row<D>(p.part_o, p.part_m, p.part_l, at, p.max_partitions - parts.first, lane, mp, lp, o_early);
+    reduce_combine_row<T, D>(static_cast<T*>(p.out), p.part_o, p.part_m, p.part_l, at, row,
+                             parts.last - parts.first + 1, mp, lp, o_early, lane);
   }
 }
 
-template <typename T, typename C, int D>
-__global__ void __launch_bounds__(128) pkv_scored_row_kernel(const DecodeParams p, const ScoreParams sc, int block_size) {
-  pdl_begin();
-  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, s = blockIdx.z;
-  const int i = blockIdx.x * 4 + warp;
-  const bool reporter = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
-  const int ctx = clamp_context(p, s, reporter);
-  int q0 = 0;
-  const int q_len = scored_query_len(sc, s, ctx, q0);
-  if (q_len < 0 && reporter) atomicOr(p.err, PKV_DEVERR_QUERY);
-  if (i >= q_len) return;
-  const int t = q0 + i, pos = ctx - q_len + i, g = h / p.group;
-  const size_t row = (size_t)t * p.num_heads + h;
-  int lo, hi;
-  scored_span(sc, t, pos, ctx, lo, hi);
-  const float slope = sc.slopes ? sc.slopes[h] * 1.4426950408889634f : 0.f;
-  float q[DPL], acc[DPL], m = -INFINITY, l = 0.f;
-  load_dims<D, T>(q, static_cast<const unsigned char*>(p.query) + row * D * 2, lane);
-#pragma unroll
-  for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];
-    if ((unsigned)phys >= (unsigned)p.num_blocks) {
-      if (lane == 0) atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-      continue;
-    }
-    const size_t at = (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB;
-    float k[DPL], v[DPL], d = 0.f;
-    load_dims<D, C>(k, p.key_cache + at, lane);
-    load_dims<D, C>(v, p.value_cache + at, lane);
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) d = fmaf(q[e], k[e], d);
-    const float x = score_value(sc, warp_sum(d), p.scale_log2) - slope * fabsf((float)(pos - j));
-    const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = fast_exp2(m - ms), w = fast_exp2(x - ms);
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
-    m = mn;
+// How a call runs: partitions of P tokens, np per sequence, and what workspace that needs.
+struct ScoredPlan {
+  int row_tiles;    // row tiles per kv head
+  int P, np;
+  size_t partials;  // bytes
+};
+
+constexpr int kScoredPartition = 1024, kScoredPartitionLong = 2048, kScoredLong = 8192;
+
+// The tokens that a sequence's partitions must cover: its context, or what a window leaves visible to its
+// query tokens (from the start of the first visible block).
+long long scored_span_bound(int block_size, int max_query_len, int max_context_len, int window) {
+  const long long w = (long long)window + max_query_len - 1 + block_size - 1;
+  return window > 0 && w < max_context_len ? w : max_context_len;
+}
+
+ScoredPlan scored_plan(int num_query_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int max_query_len, int max_context_len, int window, int partition_size) {
+  ScoredPlan pl{};
+  const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
+  pl.row_tiles = (int)((rows + 7) / 8);
+  const long long span = scored_span_bound(block_size, max_query_len, max_context_len, window);
+  if (partition_size) {
+    pl.P = partition_size;
+  } else {
+    // the nearest number of partitions of the usual size, of equal length
+    const int p0 = span > kScoredLong ? kScoredPartitionLong : kScoredPartition;
+    const long long n = span > p0 ? (span + p0 / 2) / p0 : 1;
+    long long P = ((span + n - 1) / n + block_size - 1) / block_size * block_size;
+    if (P > (long long)kMaxPartitionBlocks * block_size) P = (long long)kMaxPartitionBlocks * block_size;
+    pl.P = P < block_size ? block_size : (int)P;
   }
-  const float inv = l != 0.f ? p.v_scale / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * DPL);
-#pragma unroll
-  for (int e = 0; e < DPL / 2; ++e) dst[e] = Elem<T>::pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  const long long np = (span + pl.P - 1) / pl.P;
+  pl.np = np < 1 ? 1 : (int)np;
+  pl.partials = pl.np > 1 ? (size_t)num_query_tokens * num_heads * pl.np * (head_dim + 2) * sizeof(float) : 0;
+  return pl;
 }
 
 // Everything a call passes, under the header's names.
@@ -129,18 +133,35 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if (!decode && c.max_query_len > c.max_context_len)
     return fail(PKV_ERR_INVALID_ARG, "max_query_len %d exceeds max_context_len %d", c.max_query_len,
                 c.max_context_len);
+  if (c.partition_size < 0) return fail(PKV_ERR_INVALID_ARG, "partition_size < 0");
+  if (c.partition_size && (c.partition_size % c.block_size || c.partition_size > kMaxPartitionBlocks * c.block_size))
+    return fail(PKV_ERR_UNSUPPORTED, "partition_size %d must be a multiple of block_size in [%d, %d]",
+                c.partition_size, c.block_size, kMaxPartitionBlocks * c.block_size);
   if (c.num_seqs > 65535 || c.num_heads > 65535)
     return fail(PKV_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  if (c.max_query_len > 65535 * kReduceTokens)
+    return fail(PKV_ERR_UNSUPPORTED, "max_query_len must be <= %d", 65535 * kReduceTokens);
+  if (c.max_context_len > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "max_context_len must be <= 2^30");
   if ((long long)c.num_blocks * c.num_kv_heads * c.block_size >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "pool rows num_blocks * num_kv_heads * block_size must be < 2^31");
   if ((long long)c.num_query_tokens * c.num_heads >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "num_query_tokens * num_heads must be < 2^31");
+  const ScoredPlan pl = scored_plan(c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
+                                    c.max_query_len, c.max_context_len, c.window, c.partition_size);
+  if ((long long)pl.np * pl.row_tiles >= (1LL << 31))
+    return fail(PKV_ERR_UNSUPPORTED, "partitions * row tiles must be < 2^31");
   if (c.num_seqs == 0 || c.num_query_tokens == 0 || c.max_query_len == 0) return PKV_OK;
   if (!c.out || !c.query || !c.key_cache || !c.value_cache || !c.block_tables || !c.context_lens ||
       (!decode && !c.query_start_loc))
     return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(c.out, 16) || !aligned(c.query, 16) || !aligned(c.key_cache, 16) || !aligned(c.value_cache, 16))
     return fail(PKV_ERR_INVALID_ARG, "out, query and caches must be 16-byte aligned");
+  if (pl.partials) {
+    if (!c.workspace) return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes required", pl.partials);
+    if (c.workspace_bytes < pl.partials)
+      return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", c.workspace_bytes, pl.partials);
+    if (!aligned(c.workspace, 16)) return fail(PKV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+  }
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -163,6 +184,14 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   p.group = c.num_heads / c.num_kv_heads;
   p.num_blocks = c.num_blocks;
   p.ctx_limit = c.max_context_len;
+  p.partition_size = pl.P;
+  p.max_partitions = pl.np;
+  if (pl.partials) {
+    const size_t n = (size_t)c.num_query_tokens * c.num_heads * pl.np;
+    p.part_o = static_cast<float*>(c.workspace);
+    p.part_m = p.part_o + n * c.head_dim;
+    p.part_l = p.part_m + n;
+  }
   ScoreParams sc{};
   sc.slopes = c.alibi_slopes;
   sc.key_begin = c.key_begin;
@@ -171,22 +200,38 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   sc.window = c.window;
   sc.num_query_tokens = c.num_query_tokens;
   sc.max_query_len = c.max_query_len;
+  sc.row_tiles = pl.row_tiles;
   if (c.softcap > 0.f) {
     sc.cap_in = scale / c.softcap;
     sc.cap_out = c.softcap * 1.4426950408889634f;
   }
-  const dim3 grid((unsigned)((c.max_query_len + 3) / 4), (unsigned)c.num_heads, (unsigned)c.num_seqs);
-  auto run = [&](auto kern) { return launch_kernel(kern, grid, dim3(128), 0, c.stream, p, sc, (int)c.block_size); };
-  using F = __half;
-  using B = __nv_bfloat16;
-  using E = __nv_fp8_e4m3;
-  if (c.fp8)
-    e = c.dtype == PKV_F16 ? run(pkv_scored_row_kernel<F, E, 128>) : run(pkv_scored_row_kernel<B, E, 128>);
-  else if (c.head_dim == 128)
-    e = c.dtype == PKV_F16 ? run(pkv_scored_row_kernel<F, F, 128>) : run(pkv_scored_row_kernel<B, B, 128>);
-  else
-    e = c.dtype == PKV_F16 ? run(pkv_scored_row_kernel<F, F, 64>) : run(pkv_scored_row_kernel<B, B, 64>);
+  CUtensorMap kmap, vmap;
+  memset(&kmap, 0, sizeof kmap);
+  memset(&vmap, 0, sizeof vmap);
+  const long long pool_rows = (long long)c.num_blocks * c.num_kv_heads * c.block_size;
+  const pkv_dtype_t cache_dtype = c.fp8 ? PKV_FP8_E4M3 : c.dtype;
+  const bool one_copy = !c.fp8 && c.head_dim == 128 && tile_one_copy();
+  if (one_copy ? !make_pool_map_tc(&kmap, c.key_cache, pool_rows, c.block_size, c.dtype) ||
+                     !make_pool_map_tc(&vmap, c.value_cache, pool_rows, c.block_size, c.dtype)
+               : !make_pool_map(&kmap, c.key_cache, pool_rows, c.head_dim, c.block_size, cache_dtype) ||
+                     !make_pool_map(&vmap, c.value_cache, pool_rows, c.head_dim, c.block_size, cache_dtype))
+    return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
+  const bool f16 = c.dtype == PKV_F16;
+  e = c.fp8 ? scored_cols_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
+            : scored_cols_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
+  if (pl.np > 1) {
+    const dim3 grid((unsigned)c.num_seqs, (unsigned)((c.num_heads + kReduceRows - 1) / kReduceRows),
+                    (unsigned)((c.max_query_len + kReduceTokens - 1) / kReduceTokens));
+    auto reduce = [&](auto kern) {
+      return launch_kernel(kern, grid, dim3(32 * kReduceRows), 0, c.stream, p, sc, (int)c.block_size);
+    };
+    if (c.head_dim == 128)
+      e = f16 ? reduce(pkv_scored_reduce_kernel<__half, 128>) : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 128>);
+    else
+      e = f16 ? reduce(pkv_scored_reduce_kernel<__half, 64>) : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 64>);
+    if (e != cudaSuccess) return cuda_fail(e, "scored reduce launch");
+  }
   return PKV_OK;
 }
 
@@ -200,9 +245,12 @@ extern "C" {
 size_t paged_attention_scored_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
                                              int32_t head_dim, int32_t block_size, int32_t max_query_len,
                                              int32_t max_context_len, int32_t window, int32_t partition_size) {
-  (void)num_query_tokens, (void)num_heads, (void)num_kv_heads, (void)head_dim, (void)block_size;
-  (void)max_query_len, (void)max_context_len, (void)window, (void)partition_size;
-  return 0;
+  if (num_query_tokens <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+      block_size <= 0 || max_query_len <= 0 || max_context_len < 0 || window < 0 || partition_size < 0)
+    return 0;
+  return scored_plan(num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len, max_context_len,
+                     window, partition_size)
+      .partials;
 }
 
 pkv_status_t paged_attention_decode_scored(void* out, const void* query, const void* key_cache,

@@ -22,8 +22,10 @@ struct ScoreParams {
   int window = 0;                       // keys p - window + 1 .. are visible; 0: no window
   int num_query_tokens = 0;             // host bound on query_start_loc entries
   int max_query_len = 1;                // host bound on every q_len
-  float cap_in = 0.f;                   // scale / softcap (0: no cap)
-  float cap_out = 0.f;                  // softcap * log2(e)
+  float cap_in = 0.f;                   // scale / softcap
+  float cap_out = 0.f;                  // softcap * log2(e); 0: no cap
+  int row_tiles = 1;                    // row tiles per (partition, kv head, sequence)
+  const int32_t* order = nullptr;       // if set, the sequence of grid index z (longest context first)
 };
 
 // tanh(z): below 1 an odd polynomial, a minimax fit of tanh(z) / z in z^2 on [0, 1] (relative error 5e-8);
@@ -41,11 +43,6 @@ __device__ __forceinline__ float score_tanh(float z) {
   const float e = fast_exp2(z * 2.8853900817779268f);  // e^(2z): infinity gives 1, 0 gives -1
   const float far = 1.f - __fdividef(2.f, e + 1.f);
   return u < 1.f ? q * z : far;
-}
-
-// The score, in the base-2 domain, of a raw product `s` (without scale): sl2 = scale * log2(e).
-__device__ __forceinline__ float score_value(const ScoreParams& sc, float s, float sl2) {
-  return sc.cap_in != 0.f ? sc.cap_out * score_tanh(s * sc.cap_in) : s * sl2;
 }
 
 // q_len of sequence s with (clamped) context ctx and its first query row q0; -1 if query_start_loc is
@@ -69,6 +66,105 @@ __device__ __forceinline__ void scored_span(const ScoreParams& sc, int t, int p,
   hi = p + 1;
   if (sc.key_end) hi = min(sc.key_end[t], ctx);
   hi = max(hi, lo);
+}
+
+// A sequence's partitions: partition k holds the positions [base + k P, base + (k + 1) P), where base is the
+// start of the block of the first position that the window leaves visible to any of its query tokens (0
+// without a window). So a window costs as many partitions as it spans, wherever it lies in the context.
+__device__ __forceinline__ int scored_base(const ScoreParams& sc, int ctx, int q_len, int block_size) {
+  const int p0 = ctx - q_len;  // position of the first query token
+  return sc.window > 0 && p0 >= sc.window ? (p0 - sc.window + 1) / block_size * block_size : 0;
+}
+
+// The partitions first .. last of a row that sees [lo, hi) (lo >= base); last < first: it sees nothing. A row
+// of at most one partition is written to the output directly, by partition 0 if it is empty.
+struct RowParts {
+  int first, last;
+  __device__ __forceinline__ bool direct() const { return last <= first; }
+  __device__ __forceinline__ bool in(int part) const {
+    return last < first ? part == 0 : first <= part && part <= last;
+  }
+};
+__device__ __forceinline__ RowParts row_parts(int lo, int hi, int base, int P) {
+  if (hi <= lo) return {0, -1};
+  return {(lo - base) / P, (hi - 1 - base) / P};
+}
+
+// This lane's D / 32 dims of a stored row (16-bit or E4M3 codes).
+template <int D, typename C>
+__device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned char* row, int lane) {
+  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB;
+#pragma unroll
+  for (int e = 0; e < DPL / 2; ++e) {
+    const unsigned char* at = row + (lane * DPL + 2 * e) * EB;
+    const float2 f = CacheFmt<C>::pair(EB == 1 ? *reinterpret_cast<const uint16_t*>(at)
+                                               : *reinterpret_cast<const uint32_t*>(at));
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
+  }
+}
+
+// One row over the keys [a, b) on one warp, key by key, its lanes holding D / 32 dims each: (m, l) and the
+// output normalised by l. The tiles multiply every key of a tile with every row, a masked one with weight 0,
+// and 0 times a NaN or infinite value is NaN: a tile's row that comes out non-finite is computed again here,
+// where a masked key is not touched. So only batches that hold such values pay for it.
+template <typename T, typename C, int D>
+__device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams& sc, size_t row, int s, int h,
+                                        int pos, int a, int b, int block_size, int lane, float& m, float& l,
+                                        float (&o)[D / 32]) {
+  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB;
+  const int g = h / p.group;
+  const float slope = sc.slopes ? sc.slopes[h] * 1.4426950408889634f : 0.f;
+  float q[DPL];
+  load_dims<D, T>(q, static_cast<const unsigned char*>(p.query) + row * D * 2, lane);
+#pragma unroll
+  for (int e = 0; e < DPL; ++e) o[e] = 0.f;
+  m = -INFINITY;
+  l = 0.f;
+  for (int j = a; j < b; ++j) {
+    const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];
+    if ((unsigned)phys >= (unsigned)p.num_blocks) continue;  // (reported by the tile)
+    const size_t at = (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB;
+    float k[DPL], v[DPL], d = 0.f;
+    load_dims<D, C>(k, p.key_cache + at, lane);
+    load_dims<D, C>(v, p.value_cache + at, lane);
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) d = fmaf(q[e], k[e], d);
+    d = warp_sum(d);
+    const float x = (sc.cap_out != 0.f ? sc.cap_out * score_tanh(d * sc.cap_in) : d * p.scale_log2) -
+                    slope * fabsf((float)(pos - j));
+    const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
+    const float f = fast_exp2(m - ms), w = fast_exp2(x - ms);
+    l = fmaf(l, f, w);
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) o[e] = fmaf(o[e], f, w * v[e]);
+    m = mn;
+  }
+  const float inv = l != 0.f ? p.v_scale / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < DPL; ++e) o[e] *= inv;
+  if (l != l) m = 0.f;  // (a partial with m = -inf would be left out of the merge)
+}
+
+// The row's result of one partition: the output itself, or its partial.
+template <typename T, int D>
+__device__ __forceinline__ void store_row(const DecodeParams& p, size_t row, int part, bool direct, int lane,
+                                          float m, float l, const float (&o)[D / 32]) {
+  constexpr int DPL = D / 32;
+  if (direct) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * DPL);
+#pragma unroll
+    for (int e = 0; e < DPL / 2; ++e) dst[e] = Elem<T>::pack2(o[2 * e], o[2 * e + 1]);
+  } else {
+    const size_t at = row * p.max_partitions + part;
+    float2* dst = reinterpret_cast<float2*>(p.part_o + at * D + lane * DPL);
+#pragma unroll
+    for (int e = 0; e < DPL / 2; ++e) dst[e] = make_float2(o[2 * e], o[2 * e + 1]);
+    if (lane == 0) {
+      p.part_m[at] = m;
+      p.part_l[at] = l;
+    }
+  }
 }
 
 }  // namespace pkv
