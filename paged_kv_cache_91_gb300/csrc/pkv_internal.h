@@ -72,6 +72,14 @@ cudaError_t scored_cols_16(const DecodeParams& p, const ScoreParams& sc, const C
 cudaError_t scored_cols_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
 
+// The same on the tensor-memory tile; the pool through make_pool_map_tc (16-bit, head_dim 128), make_pool_map
+// (16-bit, head_dim 64) or make_pool_map_fp8_rows.
+cudaError_t scored_tc_16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, bool f16, int head_dim, int block_size, int num_seqs,
+                         cudaStream_t stream);
+cudaError_t scored_tc_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
+
 // Tensor maps of the pool (cuTensorMapEncodeTiled); false if the driver refuses.
 bool make_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int block_size,
                    pkv_dtype_t dtype);

@@ -42,11 +42,15 @@ __global__ void __launch_bounds__(32 * kReduceRows)
 
 // How a call runs: partitions of P tokens, np per sequence, and what workspace that needs.
 struct ScoredPlan {
+  bool tensor;      // the tensor-memory tile, 256 rows a CTA (else the 8-column one)
   int row_tiles;    // row tiles per kv head
   int P, np;
   size_t partials;  // bytes
 };
 
+// Rows per kv head from which the tensor-memory tile runs (one number for 16-bit and FP8 pools: the workspace
+// size does not know the pool's type).
+constexpr int kScoredTensorRows = 17;
 constexpr int kScoredPartition = 1024, kScoredPartitionLong = 2048, kScoredLong = 8192;
 
 // The tokens that a sequence's partitions must cover: its context, or what a window leaves visible to its
@@ -60,10 +64,14 @@ ScoredPlan scored_plan(int num_query_tokens, int num_heads, int num_kv_heads, in
                        int max_query_len, int max_context_len, int window, int partition_size) {
   ScoredPlan pl{};
   const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
-  pl.row_tiles = (int)((rows + 7) / 8);
+  pl.tensor = rows >= kScoredTensorRows;
+  pl.row_tiles = (int)(pl.tensor ? (rows + 255) / 256 : (rows + 7) / 8);
   const long long span = scored_span_bound(block_size, max_query_len, max_context_len, window);
   if (partition_size) {
     pl.P = partition_size;
+  } else if (pl.tensor) {
+    pl.P = (int)((span + block_size - 1) / block_size * block_size);
+    if (pl.P < block_size) pl.P = block_size;
   } else {
     // the nearest number of partitions of the usual size, of equal length
     const int p0 = span > kScoredLong ? kScoredPartitionLong : kScoredPartition;
@@ -210,15 +218,21 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   memset(&vmap, 0, sizeof vmap);
   const long long pool_rows = (long long)c.num_blocks * c.num_kv_heads * c.block_size;
   const pkv_dtype_t cache_dtype = c.fp8 ? PKV_FP8_E4M3 : c.dtype;
-  const bool one_copy = !c.fp8 && c.head_dim == 128 && tile_one_copy();
-  if (one_copy ? !make_pool_map_tc(&kmap, c.key_cache, pool_rows, c.block_size, c.dtype) ||
+  const bool one_copy = !c.fp8 && c.head_dim == 128 && (pl.tensor || tile_one_copy());
+  if (c.fp8 && pl.tensor ? !make_pool_map_fp8_rows(&kmap, c.key_cache, pool_rows, c.block_size) ||
+                               !make_pool_map_fp8_rows(&vmap, c.value_cache, pool_rows, c.block_size)
+      : one_copy ? !make_pool_map_tc(&kmap, c.key_cache, pool_rows, c.block_size, c.dtype) ||
                      !make_pool_map_tc(&vmap, c.value_cache, pool_rows, c.block_size, c.dtype)
                : !make_pool_map(&kmap, c.key_cache, pool_rows, c.head_dim, c.block_size, cache_dtype) ||
                      !make_pool_map(&vmap, c.value_cache, pool_rows, c.head_dim, c.block_size, cache_dtype))
     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
   const bool f16 = c.dtype == PKV_F16;
-  e = c.fp8 ? scored_cols_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
-            : scored_cols_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
+  if (pl.tensor)
+    e = c.fp8 ? scored_tc_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
+              : scored_tc_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
+  else
+    e = c.fp8 ? scored_cols_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
+              : scored_cols_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
   if (pl.np > 1) {
     const dim3 grid((unsigned)c.num_seqs, (unsigned)((c.num_heads + kReduceRows - 1) / kReduceRows),

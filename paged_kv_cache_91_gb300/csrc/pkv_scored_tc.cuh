@@ -1,0 +1,581 @@
+// Scored paged attention with many rows per kv head, on the fifth-generation tensor cores (tcgen05).
+//
+// One CTA per SM takes up to 256 (query token, head) rows of a (partition, kv head, sequence) -- row r is query
+// token r / G, head kvh * G + r % G -- and walks the keys that any of them sees in tiles of 128 tokens
+// (128 / block_size pool blocks). Its two streams of 128 rows each compute, tile by tile,
+//   S = Q . K^T        M 128, N 128, K = head_dim       -> tensor memory (fp32)
+//   P = exp2(score(S) - m)   one thread per row, in two halves of 64 keys, 16-bit, over S's columns
+//   O += P . V         M 128, N = head_dim, K 64 a half   A from tensor memory
+// The streams share every K and V tile (read once per 256 rows), and one's products run while the other's
+// threads exponentiate. A CTA with at most 128 rows gives both streams the same rows: stream w then takes every
+// second tile, and their (m, l, O) are merged at the end.
+//
+// What bounds it: per 256 x 128 scores the tensor cores need about 2048 cycles (head_dim 128) and the shared
+// memory port as many (Q and K twice, V twice, the copies once); the exponentials take 1 special-function
+// operation a score and the scores 4 to 8 fp32 operations (cap), which is of the same size. So the streams
+// overlap the two, and a score is kept to few instructions: tiles that every row sees whole skip the masks,
+// and the tanh is a polynomial where the tile's scores stay well below the cap.
+//
+// Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 and 11 copy the
+// blocks of K and V tiles, half of each tile a warp (a copy takes about 100 cycles to issue), into a ring of
+// tile slots in the order K0 V0 K1 V1 ...; FP8 pool: 12-15 widen a tile's codes to f16 in place.
+// Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set PKV_DEVERR_TIMEOUT and
+// write zeros.
+#pragma once
+
+#include <type_traits>
+
+#include "pkv_mq_tc.cuh"
+#include "pkv_scored.cuh"
+
+namespace pkv {
+
+template <typename T, int D, int BS, bool F8>
+struct ScoredTcShape {
+  static constexpr int ROWS = 128;           // rows per stream (M)
+  static constexpr int NT = 128;             // tokens per tile
+  static constexpr int NBT = NT / BS;        // pool blocks per tile
+  static constexpr int DH = D / 64;          // 128-byte halves of a 16-bit row
+  static constexpr int ATOM = DH * 1024;     // 8 tokens: their columns 0..63, then 64..127
+  static constexpr int TILE = NT / 8 * ATOM; // bytes of a K or V tile slot
+  static constexpr int QT = DH * ROWS * 128; // bytes of a stream's Q
+  static constexpr int NS = D == 128 ? 5 : 8;  // tile slots
+  static constexpr int HALF = TILE / 2;      // FP8 pool: a tile's codes land in its slot's upper half
+  static constexpr int OFF_RING = 2 * QT;
+  static constexpr int OFF_BARS = OFF_RING + NS * TILE;
+  // barriers: full[8], empty[8], raw[8] per slot; per stream q_full, s_full, p_full[2], pv_half, pv_done, fin
+  static constexpr int NBARS = 24 + 14;
+  static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;  // tensor-memory base, abort flag, key range, row state
+  static constexpr int OFF_ML = OFF_MISC + 16;           // stream 1's (m, l) in a CTA of shared rows
+  static constexpr int SMEM = OFF_ML + 2 * ROWS * 4;
+  static constexpr int S_COL = 0, O_COL = 256;  // tensor memory: stream w's S at 128 w, its O at 256 + 128 w
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int MMA_WARP = 8, COPY_WARP = 10, WIDEN_WARP = 12;
+  static constexpr int THREADS = (F8 ? 16 : 12) * 32;
+  static_assert(SMEM <= 232448 - 1024, "one CTA's shared memory");
+  static_assert(NBT >= 4 && NBT <= 16, "blocks per tile");
+  static_assert(!F8 || D == 128, "an FP8 pool: head_dim 128");
+  static_assert(2 * ROWS * D * 2 <= NS * TILE, "the merge of the streams stages one O in the ring");
+};
+
+// Whether every thread of the four widening warps says yes.
+__device__ __forceinline__ bool widen_agree(bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(yes ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// FP8 pool: a widening warp's 32 tokens (4 atoms) of a tile. The whole tile is read into registers (all four
+// warps, then a barrier) before anything is written, because the f16 atoms overwrite the codes. Lane (t = lane
+// / 4, q = lane % 4) takes codes 32 q .. of token 8 a + t; the orders keep 8-lane phases on distinct banks.
+__device__ __forceinline__ void scored_widen(unsigned char* slot, int half, int w, int lane) {
+  const unsigned char* src = slot + half + w * 32 * 128;
+  const int t8 = lane >> 2, q = lane & 3;
+  const int h0 = (t8 & 1) * 16, h1 = 16 - h0;
+  uint4 c[4][2];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const unsigned char* row = src + (8 * a + t8) * 128 + 32 * q;
+    const uint4 x = *reinterpret_cast<const uint4*>(row + h0);
+    const uint4 y = *reinterpret_cast<const uint4*>(row + h1);
+    c[a][0] = h0 ? y : x;
+    c[a][1] = h0 ? x : y;
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");  // the four widening warps
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const uint32_t x[8] = {c[a][0].x, c[a][0].y, c[a][0].z, c[a][0].w, c[a][1].x, c[a][1].y, c[a][1].z, c[a][1].w};
+    unsigned char* row = slot + (4 * w + a) * 2048 + (q >> 1) * 1024 + t8 * 128;
+    const bool rot = (q >> 1) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int kk = rot ? (k ^ 2) : k;
+      uint32_t h[4];
+      e4m3x4_to_f16x2(rot ? x[2 * (k ^ 2)] : x[2 * k], h[0], h[1]);
+      e4m3x4_to_f16x2(rot ? x[2 * (k ^ 2) + 1] : x[2 * k + 1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(row + ((((q & 1) * 4 + kk) ^ t8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+template <typename T, int D, int BS, bool F8>
+__global__ void __launch_bounds__(F8 ? 512 : 384, 1)
+    pkv_scored_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ ScoreParams sc,
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  pdl_begin();
+  using Sh = ScoredTcShape<T, D, BS, F8>;
+  using TP = typename std::conditional<F8, __half, T>::type;  // the MMAs' type
+  using C = typename std::conditional<F8, __nv_fp8_e4m3, T>::type;  // the cache's
+  constexpr int NT = Sh::NT, NBT = Sh::NBT, NS = Sh::NS, ROWS = Sh::ROWS;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BARS);
+  uint64_t *full = bars, *empty = bars + 8, *raw = bars + 16;
+  uint64_t* q_full = bars + 24;   // [stream]
+  uint64_t* s_full = bars + 26;   // [stream]
+  uint64_t* p_full = bars + 28;   // [stream][half]
+  uint64_t* pv_half = bars + 32;  // [stream]: the first half's PV
+  uint64_t* pv_done = bars + 34;  // [stream]: the tile's PV
+  uint64_t* fin = bars + 36;      // [stream]: everything issued
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::OFF_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* range = reinterpret_cast<int*>(tmem_slot + 2);  // first visible key, end of the visible keys
+  auto slot = [&](int it) { return smem + Sh::OFF_RING + (it % NS) * Sh::TILE; };
+
+  // the last row tiles first: with a causal limit they see the most keys
+  const int part = blockIdx.x / sc.row_tiles, rt = sc.row_tiles - 1 - (int)blockIdx.x % sc.row_tiles;
+  const int kvh = blockIdx.y;
+  const int s = sc.order ? sc.order[blockIdx.z] : (int)blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.group, P = p.partition_size;
+  const bool reporter = blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0;
+  if (smem_u32(smem) & 1023u) {  // not expected on any supported GPU; nothing is written
+    if (threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_LAYOUT);
+    return;
+  }
+  const int ctx = clamp_context(p, s, reporter);
+  int q0 = 0;
+  const int q_len = scored_query_len(sc, s, ctx, q0);
+  if (q_len < 0) {
+    if (reporter) atomicOr(p.err, PKV_DEVERR_QUERY);
+    return;
+  }
+  const long long R = (long long)q_len * G, row0 = (long long)rt * 2 * ROWS;
+  if (row0 >= R) return;
+  const int nrows = (int)min((long long)2 * ROWS, R - row0);
+  const bool shared_rows = nrows <= ROWS;  // both streams take the same rows
+  const int base = scored_base(sc, ctx, q_len, BS);
+  const int tok0 = base + part * P;
+
+  // the streams' rows: warps 0-7, thread row = its tensor-memory lane
+  const int w = warp >> 2;  // (stream, for warps 0-7)
+  const int row = 32 * (warp & 3) + lane;
+  const int rr = (shared_rows ? 0 : w * ROWS) + row;  // row within the CTA
+  const bool active = warp < 8 && rr < nrows;
+  const int ti = active ? (int)((row0 + rr) / G) : 0;  // query token within the sequence
+  const int h = kvh * G + (active ? (int)((row0 + rr) % G) : 0);
+  const int pos = ctx - q_len + ti;
+  int lo = 0, hi = 0;
+  if (active) scored_span(sc, q0 + ti, pos, ctx, lo, hi);
+  const RowParts parts = row_parts(lo, hi, base, P);
+
+  // the CTA's keys: from its rows' first to their last visible one, within the partition
+  int c0, c1;
+  if (!sc.key_begin && !sc.key_end) {  // the first row's first, the last row's last
+    int unused;
+    scored_span(sc, 0, ctx - q_len + (int)(row0 / G), ctx, c0, unused);
+    scored_span(sc, 0, ctx - q_len + (int)((row0 + nrows - 1) / G), ctx, unused, c1);
+  } else {
+    if (threadIdx.x == 0) {
+      range[0] = INT32_MAX;
+      range[1] = 0;
+    }
+    __syncthreads();
+    if (warp < 8) {
+      int a = hi > lo ? lo : INT32_MAX, b = hi > lo ? hi : 0;
+      a = __reduce_min_sync(kFull, a);
+      b = __reduce_max_sync(kFull, b);
+      if (lane == 0) {
+        atomicMin(range, a);
+        atomicMax(range + 1, b);
+      }
+    }
+    __syncthreads();
+    c0 = range[0];
+    c1 = range[1];
+  }
+  c0 = max(c0, tok0);
+  c1 = min(c1, tok0 + P);
+  T* out_row = static_cast<T*>(p.out) + ((size_t)(q0 + ti) * p.num_heads + h) * D;
+  if (c1 <= c0) {  // no key: partition 0 writes the zeros of rows that see nothing
+    if (part == 0 && active && parts.last < parts.first)
+      for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out_row + d) = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const int blk0 = c0 / BS, nblk = (c1 + BS - 1) / BS - blk0;
+  const int ntile = (nblk + NBT - 1) / NBT;
+  const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq + blk0;
+  const int step = shared_rows ? 2 : 1;                  // a stream's tiles: first, first + step, ...
+  auto first_tile = [&](int stream) { return shared_rows ? stream : 0; };
+
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    for (int k = 0; k < NS; ++k) {
+      mbar_init(full + k, F8 ? 4 : 2);
+      mbar_init(empty + k, shared_rows ? 1 : 2);
+      mbar_init(raw + k, 2);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(q_full + k, ROWS);
+      mbar_init(s_full + k, 1);
+      mbar_init(p_full + 2 * k, ROWS);
+      mbar_init(p_full + 2 * k + 1, ROWS);
+      mbar_init(pv_half + k, 1);
+      mbar_init(pv_done + k, 1);
+      mbar_init(fin + k, 1);
+    }
+    fence_mbar_init();
+    *abort = 0;
+  }
+  if (warp == Sh::MMA_WARP) tc::alloc(tmem_slot, Sh::TMEM_COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp == Sh::COPY_WARP || warp == Sh::COPY_WARP + 1) {
+    // ---- copies: this warp's half of the blocks of item it = 2 j (K tile j) and 2 j + 1 (V tile j)
+    constexpr int NH = NBT / 2;
+    const int at = (warp - Sh::COPY_WARP) * NH + (lane & (NH - 1));  // lane < NH: block of the tile
+    uint64_t* landed = F8 ? raw : full;
+    auto load_id = [&](int j) { return lane < NH && j * NBT + at < nblk ? table[j * NBT + at] : -1; };
+    int next = load_id(0);
+    int it = 0;
+    bool ok = true;
+    for (int j = 0; ok && j < ntile; ++j) {
+      int id = next;
+      if (j + 1 < ntile) next = load_id(j + 1);
+      if (lane < NH && j * NBT + at < nblk && (unsigned)id >= (unsigned)p.num_blocks) {
+        atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+        id = -1;
+      }
+      const int n = __popc(__ballot_sync(kFull, id >= 0));
+      const int y = (id * p.num_kv_heads + kvh) * BS;  // first pool row of the block
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++it) {
+        uint64_t* bar = landed + it % NS;
+        if (it >= NS) ok = __all_sync(kFull, tc_wait(empty + it % NS, (it / NS - 1) & 1, abort));
+        if (!ok) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();  // generic stores into the slot (zeroed rows, widened codes): before the copies
+          mbar_arrive_expect_tx(bar, n * BS * (F8 ? 128 : D * 2));
+        }
+        __syncwarp();
+        if (id >= 0) {
+          if constexpr (F8)
+            tma_load_2d(slot(it) + Sh::HALF + at * BS * 128, kv ? &vmap : &kmap, 0, y, bar);
+          else if constexpr (Sh::DH == 2)
+            tma_load_4d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, 0, 0, y / 8, bar);
+          else
+            tma_load_2d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, y, bar);
+        }
+      }
+    }
+    // no copy may still be landing when the CTA leaves
+    if (lane == 0)
+      for (int k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait(landed + k % NS, (k / NS) & 1);
+  } else if (F8 && warp >= Sh::WIDEN_WARP) {
+    // ---- FP8 pool: widen each item's codes once they have landed
+    for (int it = 0; it < 2 * ntile; ++it) {
+      // (agreed among the four warps, which meet at barriers: all go on, or all leave)
+      if (!widen_agree(tc_wait(raw + it % NS, (it / NS) & 1, abort))) break;
+      if constexpr (F8) scored_widen(slot(it), Sh::HALF, warp - Sh::WIDEN_WARP, lane);
+      fence_proxy_async_smem();  // generic stores, read by the MMAs
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + it % NS);
+    }
+  } else if (warp == Sh::MMA_WARP || warp == Sh::MMA_WARP + 1) {
+    // ---- MMA issue: one thread per stream, S and PV in tile order
+    if (lane == 0) {
+      const int st = warp - Sh::MMA_WARP;
+      constexpr bool BF = std::is_same<TP, __nv_bfloat16>::value;
+      constexpr uint32_t IDESC_S = tc::idesc_f16(BF, ROWS, NT, false, false);
+      constexpr uint32_t IDESC_O = tc::idesc_f16(BF, ROWS, D, false, true);
+      const uint32_t q_addr = smem_u32(smem) + (shared_rows ? 0 : st * Sh::QT);
+      const uint32_t scol = tbase + Sh::S_COL + st * NT, ocol = tbase + Sh::O_COL + st * 128;
+      bool ok = shared_rows ? tc_wait(q_full, 0, abort) && tc_wait(q_full + 1, 0, abort) : tc_wait(q_full + st, 0, abort);
+      int n = 0;
+      for (int j = first_tile(st); ok && j < ntile; j += step, ++n) {
+        const int ik = 2 * j, iv = ik + 1;
+        if (!(ok = tc_wait(full + ik % NS, (ik / NS) & 1, abort))) break;
+        tc::fence_after_sync();
+        const uint32_t k_addr = smem_u32(slot(ik));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_f16(scol, tc::desc_sw128(q_addr + (k / 4) * (ROWS * 128) + (k % 4) * 32, 16, 1024),
+                      tc::desc_sw128(k_addr + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::ATOM), IDESC_S, k > 0);
+        tc::commit(s_full + st);
+        tc::commit(empty + ik % NS);
+        const uint32_t v_addr = smem_u32(slot(iv));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          ok = ok && tc_wait(p_full + 2 * st + hf, n & 1, abort) &&
+               (hf > 0 || tc_wait(full + iv % NS, (iv / NS) & 1, abort));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 16 keys each: 8 columns of P, two atoms of V
+            tc::mma_f16_ta(ocol, scol + hf * 64 + k * 8,
+                           tc::desc_sw128(v_addr + (hf * 4 + k) * 2 * Sh::ATOM, 1024, Sh::ATOM), IDESC_O,
+                           n > 0 || hf > 0 || k > 0);
+          tc::commit(hf ? pv_done + st : pv_half + st);
+        }
+        if (!ok) break;
+        tc::commit(empty + iv % NS);
+        // the next S overwrites this tile's P: not before its PV has read it
+        ok = tc_wait(pv_done + st, n & 1, abort);
+      }
+      tc::commit(fin + st);  // every MMA issued above has completed once this arrives
+      mbar_wait(fin + st, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- rows
+    float qscale = 1.f;  // FP8 pool, bf16 query: the 2^-k the row was scaled by
+    unsigned char* Qs = smem + (shared_rows ? 0 : w * Sh::QT);
+    // (row tile rt of 256 rows: stream w's rows are tile 2 rt + w of 128 rows)
+    const int rt128 = 2 * rt + (shared_rows ? 0 : w);
+    if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
+      // (in a CTA of shared rows both streams need the factor; both store the same Q)
+      qscale = mq_tc_fetch_q_bf16_as_f16<D, ROWS>(Qs, row, reinterpret_cast<const __nv_bfloat16*>(p.query), q0, kvh,
+                                                  rt128, q_len, G, p.num_heads);
+    } else if (!shared_rows || w == 0) {
+      mq_tc_fetch_q<T, D, ROWS>(Qs, row, reinterpret_cast<const T*>(p.query), q0, kvh, rt128, q_len, G, p.num_heads);
+      cp_async_wait_all();
+    }
+    fence_proxy_async_smem();  // generic-proxy writes, read by the S MMAs
+    mbar_arrive(q_full + w);
+    const float sl2 = p.scale_log2 * qscale;
+    const bool capped = sc.cap_out != 0.f, biased = sc.slopes != nullptr;
+    const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
+    const float slope = biased ? sc.slopes[h] * 1.4426950408889634f : 0.f;
+    const int t_first = blk0 * BS;
+    const uint32_t scol = tc::taddr(tbase, 32 * (warp & 3), Sh::S_COL + w * NT);
+    const uint32_t ocol = tc::taddr(tbase, 32 * (warp & 3), Sh::O_COL + w * 128);
+    // which blocks of a tile were copied: lane b < NBT holds block b's test (the copying warps' own)
+    auto load_ok = [&](int j) {
+      const int b = j * NBT + (lane & (NBT - 1));
+      return b < nblk ? (unsigned)table[b] < (unsigned)p.num_blocks : false;
+    };
+    constexpr uint32_t all = NBT == 32 ? 0xffffffffu : (1u << NBT) - 1u;
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    int n = 0;
+    bool next = first_tile(w) < ntile && load_ok(first_tile(w));
+    for (int j = first_tile(w); j < ntile; j += step, ++n) {
+      const uint32_t blocks = __ballot_sync(kFull, next) & all;
+      if (j + step < ntile) next = load_ok(j + step);
+      // (tensor-memory accesses are warp-wide: a warp leaves the loop as a whole)
+      ok = __all_sync(kFull, tc_wait(s_full + w, n & 1, abort));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const int tb = t_first + j * NT;  // position of the tile's first token
+      const bool edge = blocks != all || tb < c0 || tb + NT > c1;  // V rows outside the CTA's keys, or not copied
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        const int th = tb + hf * 64;
+        uint32_t sr[2][32];
+        tc::ld32(scol + hf * 64, sr[0]);
+        tc::ld32(scol + hf * 64 + 32, sr[1]);
+        tc::wait_ld();
+        float x[64];
+#pragma unroll
+        for (int t = 0; t < 64; ++t) x[t] = __uint_as_float(sr[t >> 5][t & 31]);
+        // x[t] * mul is the score in the base-2 domain; masked keys get -inf
+        float mul = sl2;
+        const bool whole = !edge && th >= lo && th + 64 <= hi;
+        if (capped) {
+          mul = 1.f;
+#pragma unroll
+          for (int t = 0; t < 64; ++t) x[t] = cap_out * score_tanh(x[t] * cap_in);
+        } else if (biased || !whole || sl2 < 0.f) {
+          mul = 1.f;
+#pragma unroll
+          for (int t = 0; t < 64; ++t) x[t] *= sl2;
+        }
+        if (biased) {
+          const float d0 = (float)(pos - th);
+#pragma unroll
+          for (int t = 0; t < 64; ++t) x[t] = fmaf(-slope, fabsf(d0 - (float)t), x[t]);
+        }
+        if (!whole) {
+          const uint32_t hb = blocks >> (hf * (NBT / 2));
+          const int a = lo - th;
+          const unsigned len = (unsigned)(hi - lo);
+#pragma unroll
+          for (int t = 0; t < 64; ++t) {
+            const bool see = (unsigned)(t - a) < len && ((hb >> (t / BS)) & 1u);
+            x[t] = see ? x[t] : -INFINITY;
+          }
+        }
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 64; ++t) mq[t & 3] = fmaxf(mq[t & 3], x[t]);
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * mul;
+        const bool move = mx > m_ref + 8.f;
+        const bool resc = move && m_ref != -INFINITY;  // O's row holds terms to rescale
+        const float f = resc ? fast_exp2(m_ref - mx) : 1.f;
+        if (move) m_ref = mx;
+        // P row as 16-bit pairs. l sums the fp32 weights before their rounding to 16 bits, which moves the
+        // result by at most the rounding unit times the row's largest |v|. A row that has seen nothing yet
+        // exponentiates against 0 (its x are -inf, or NaN, which must stay).
+        uint32_t pw[32];
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const float p0 = fast_exp2(fmaf(x[2 * u], mul, nm)), p1 = fast_exp2(fmaf(x[2 * u + 1], mul, nm));
+          pw[u] = Elem<TP>::pack2(p0, p1);
+          ls[u & 3] += p0 + p1;
+        }
+        if (__any_sync(kFull, resc)) {  // the whole warp moves its rows' O (factor 1 for rows that keep theirs)
+          // the tile before is done (its P's columns hold this S); the half before may still be multiplied
+          if (hf > 0) ok = __all_sync(kFull, tc_wait(pv_half + w, n & 1, abort));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc::ld32(ocol + c * 32, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+            tc::st32(ocol + c * 32, o);
+          }
+        }
+        l = l * f + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+        tc::st32(scol + hf * 64, pw);  // P over S
+        tc::wait_st();
+        // V rows that were not copied, or lie outside the CTA's keys, may hold anything (NaN): zero them once
+        // V has landed, since P = 0 times NaN is NaN in the MMA
+        if (edge && hf == 0) {
+          const int iv = 2 * j + 1;
+          ok = __all_sync(kFull, tc_wait(full + iv % NS, (iv / NS) & 1, abort));
+          if (!ok) break;
+          unsigned char* vs = slot(iv);
+          for (int i = threadIdx.x & 127; i < NT * 8 * Sh::DH; i += 128) {
+            const int t = i / (8 * Sh::DH), c = i % (8 * Sh::DH);
+            if (!((blocks >> (t / BS)) & 1u) || tb + t >= c1 || tb + t < c0)
+              *reinterpret_cast<uint4*>(vs + (t / 8) * Sh::ATOM + (c / 8) * 1024 + tc::sw128(t % 8, c % 8)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();  // the zeros precede the PV's reads
+        }
+        tc::fence_before_sync();
+        mbar_arrive(p_full + 2 * w + hf);
+      }
+      if (!ok) break;
+    }
+    // ---- epilogue: O / l
+    if (ok && n > 0) ok = __all_sync(kFull, tc_wait(pv_done + w, (n - 1) & 1, abort));
+    tc::fence_after_sync();
+    float f0 = 1.f, f1 = 0.f;  // factors of this stream's O and of the other's (shared rows)
+    float* stage = reinterpret_cast<float*>(smem + Sh::OFF_RING);  // [D][128]: the other stream's O
+    float* ml = reinterpret_cast<float*>(smem + Sh::OFF_ML);
+    if (shared_rows) {
+      // stream 1 hands its (m, l, O) over; every slot has been read, for both streams' PV are done
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (w == 1) {
+        ml[row] = ok && n > 0 ? m_ref : -INFINITY;
+        ml[ROWS + row] = ok && n > 0 ? l : 0.f;
+        if (ok && n > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc::ld32(ocol + c * 32, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) stage[(c * 32 + u) * ROWS + row] = __uint_as_float(o[u]);
+          }
+        } else {
+          for (int d = 0; d < D; ++d) stage[d * ROWS + row] = 0.f;
+        }
+      }
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (w == 0) {
+        const float m1 = ml[row], l1 = ml[ROWS + row];
+        const float M = fmaxf(m_ref, m1), Ms = M == -INFINITY ? 0.f : M;
+        f0 = m_ref == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_ref - Ms);
+        f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : fast_exp2(m1 - Ms);
+        l = l * f0 + l1 * f1;
+        m_ref = M;
+      }
+    }
+    ok = ok && !*abort;
+    if (!shared_rows || w == 0) {
+      const bool mine = active && parts.in(part), direct = parts.direct();
+      const size_t orow = (size_t)(q0 + ti) * p.num_heads + h;
+      // 1 / l (FP8 pool: times the value of one V code)
+      const float inv = ok && l != 0.f ? (F8 ? p.v_scale : 1.f) / l : 0.f;
+      bool fine = true;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tc::ld32(ocol + c * 32, o);
+        tc::wait_ld();
+        float v[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          v[u] = __uint_as_float(o[u]);
+          if (shared_rows) v[u] = f0 * v[u] + f1 * stage[(c * 32 + u) * ROWS + row];
+          v[u] = ok ? v[u] * inv : 0.f;
+          fine = fine && fabsf(v[u]) < INFINITY;
+        }
+        if (!mine) continue;
+        if (direct) {
+          uint4* dst = reinterpret_cast<uint4*>(out_row + c * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            dst[u] = make_uint4(Elem<T>::pack2(v[8 * u], v[8 * u + 1]), Elem<T>::pack2(v[8 * u + 2], v[8 * u + 3]),
+                                Elem<T>::pack2(v[8 * u + 4], v[8 * u + 5]), Elem<T>::pack2(v[8 * u + 6], v[8 * u + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.max_partitions + part) * D + c * 32);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        }
+      }
+      if (mine && !direct) {
+        p.part_m[orow * p.max_partitions + part] = ok ? m_ref : -INFINITY;
+        p.part_l[orow * p.max_partitions + part] = ok ? l : 0.f;
+      }
+      // rows that came out non-finite: again, key by key, on the whole warp
+      for (uint32_t redo = __ballot_sync(kFull, mine && !fine); redo; redo &= redo - 1) {
+        const int src = __ffs(redo) - 1;
+        const int rlo = __shfl_sync(kFull, lo, src), rhi = __shfl_sync(kFull, hi, src);
+        const int rpos = __shfl_sync(kFull, pos, src), rh = __shfl_sync(kFull, h, src);
+        const int rti = __shfl_sync(kFull, ti, src);
+        const bool rdirect = __shfl_sync(kFull, (int)direct, src);
+        const size_t at = (size_t)(q0 + rti) * p.num_heads + rh;
+        float m, ll, o[D / 32];
+        scored_row<T, C, D>(p, sc, at, s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, m, ll, o);
+        store_row<T, D>(p, at, part, rdirect, lane, m, ll, o);
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*abort && threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+  if (warp == Sh::MMA_WARP) {
+    tc::fence_after_sync();
+    tc::dealloc(tbase, Sh::TMEM_COLS);
+  }
+}
+
+template <typename T, int D, int BS, bool F8>
+cudaError_t launch_scored_tc(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, int num_seqs, cudaStream_t stream) {
+  using Sh = ScoredTcShape<T, D, BS, F8>;
+  auto kern = pkv_scored_tc_kernel<T, D, BS, F8>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  const dim3 grid((unsigned)p.max_partitions * (unsigned)sc.row_tiles, (unsigned)p.num_kv_heads, (unsigned)num_seqs);
+  return launch_kernel(kern, grid, dim3(Sh::THREADS), Sh::SMEM, stream, p, sc, kmap, vmap);
+}
+
+}  // namespace pkv
