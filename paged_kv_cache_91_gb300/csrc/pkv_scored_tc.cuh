@@ -30,6 +30,68 @@
 
 namespace pkv {
 
+// Pairs of fp32 values in one 64-bit register pair: one instruction for two operations.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The largest of 64 values held as pairs.
+__device__ __forceinline__ float max64(const f32x2 (&x)[32]) {
+  float m[4], a, b;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    unpair2(x[k], a, b);
+    m[k] = fmaxf(a, b);
+  }
+#pragma unroll
+  for (int k = 4; k < 32; ++k) {
+    unpair2(x[k], a, b);
+    m[k & 3] = max3(m[k & 3], a, b);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// The largest of their negatives.
+__device__ __forceinline__ float max64neg(const f32x2 (&x)[32]) {
+  float m[4], a, b;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    unpair2(x[k], a, b);
+    m[k] = fmaxf(-a, -b);
+  }
+#pragma unroll
+  for (int k = 4; k < 32; ++k) {
+    unpair2(x[k], a, b);
+    m[k & 3] = max3(m[k & 3], -a, -b);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 template <typename T, int D, int BS, bool F8>
 struct ScoredTcShape {
   static constexpr int ROWS = 128;           // rows per stream (M)
@@ -70,6 +132,17 @@ __device__ __forceinline__ bool widen_agree(bool yes) {
       : "r"(yes ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+
+// x -= slope |d0 - t| for the half's 64 keys t.
+__device__ __forceinline__ void add_bias(f32x2 (&x)[32], float slope, int d0) {
+  const float d = (float)d0;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    float a, b;
+    unpair2(x[u], a, b);
+    x[u] = pair2(fmaf(-slope, fabsf(d - (float)(2 * u)), a), fmaf(-slope, fabsf(d - (float)(2 * u + 1)), b));
+  }
 }
 
 // FP8 pool: a widening warp's 32 tokens (4 atoms) of a tile. The whole tile is read into registers (all four
@@ -346,6 +419,21 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     const bool capped = sc.cap_out != 0.f, biased = sc.slopes != nullptr;
     const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
     const float slope = biased ? sc.slopes[h] * 1.4426950408889634f : 0.f;
+    // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
+    // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers leave fp32's range.)
+    f32x2 cc[4];
+    float near2 = -1.f;  // the largest x^2 that it is for
+    {
+      const float z2 = cap_in * cap_in;
+      float c = cap_out * cap_in;
+      const float fit[4] = {0.999999456f, -0.333263179f, 0.131902965f, -0.0444022226f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cc[k] = pair2(c * fit[k], c * fit[k]);
+        c *= z2;
+      }
+      if (z2 < 1e6f && z2 > 1e-18f) near2 = 0.25f / z2;
+    }
     const int t_first = blk0 * BS;
     const uint32_t scol = tc::taddr(tbase, 32 * (warp & 3), Sh::S_COL + w * NT);
     const uint32_t ocol = tc::taddr(tbase, 32 * (warp & 3), Sh::O_COL + w * 128);
@@ -375,40 +463,66 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         tc::ld32(scol + hf * 64, sr[0]);
         tc::ld32(scol + hf * 64 + 32, sr[1]);
         tc::wait_ld();
-        float x[64];
+        f32x2 x[32];  // keys 2 u and 2 u + 1 of the half
 #pragma unroll
-        for (int t = 0; t < 64; ++t) x[t] = __uint_as_float(sr[t >> 5][t & 31]);
-        // x[t] * mul is the score in the base-2 domain; masked keys get -inf
-        float mul = sl2;
+        for (int u = 0; u < 32; ++u)
+          x[u] = pair2(__uint_as_float(sr[u >> 4][(2 * u) & 31]), __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]));
+        // x * mul is the score in the base-2 domain; masked keys get -inf
+        float mul = 1.f;
         const bool whole = !edge && th >= lo && th + 64 <= hi;
         if (capped) {
-          mul = 1.f;
+          const float top = max64(x), bottom = -max64neg(x);
+          if (__all_sync(kFull, fmaxf(top * top, bottom * bottom) <= near2)) {  // the warp's scores: at most half the cap
 #pragma unroll
-          for (int t = 0; t < 64; ++t) x[t] = cap_out * score_tanh(x[t] * cap_in);
-        } else if (biased || !whole || sl2 < 0.f) {
-          mul = 1.f;
+            for (int u = 0; u < 32; ++u) {
+              const f32x2 sq = mul2(x[u], x[u]);
+              x[u] = mul2(x[u], fma2(sq, fma2(sq, fma2(sq, cc[3], cc[2]), cc[1]), cc[0]));
+            }
+          } else {
 #pragma unroll
-          for (int t = 0; t < 64; ++t) x[t] *= sl2;
-        }
-        if (biased) {
-          const float d0 = (float)(pos - th);
+            for (int u = 0; u < 32; ++u) {
+              float a, b;
+              unpair2(x[u], a, b);
+              x[u] = pair2(cap_out * score_tanh(a * cap_in), cap_out * score_tanh(b * cap_in));
+            }
+          }
+          if (biased) add_bias(x, slope, pos - th);
+        } else if (biased) {
+          // keys up to the token's own position: -slope (p - j) is linear in j
+          if (__all_sync(kFull, pos >= th + 63)) {
+            const f32x2 m2 = pair2(sl2, sl2), s2 = pair2(slope, slope);
+            const float d0 = -slope * (float)(pos - th);
+            const f32x2 base2 = pair2(d0, d0);
 #pragma unroll
-          for (int t = 0; t < 64; ++t) x[t] = fmaf(-slope, fabsf(d0 - (float)t), x[t]);
+            for (int u = 0; u < 32; ++u)
+              x[u] = fma2(x[u], m2, fma2(s2, pair2((float)(2 * u), (float)(2 * u + 1)), base2));
+          } else {
+            const f32x2 m2 = pair2(sl2, sl2);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], m2);
+            add_bias(x, slope, pos - th);
+          }
+        } else if (!whole || sl2 < 0.f) {
+          const f32x2 m2 = pair2(sl2, sl2);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], m2);
+        } else {
+          mul = sl2;
         }
         if (!whole) {
           const uint32_t hb = blocks >> (hf * (NBT / 2));
           const int a = lo - th;
           const unsigned len = (unsigned)(hi - lo);
 #pragma unroll
-          for (int t = 0; t < 64; ++t) {
-            const bool see = (unsigned)(t - a) < len && ((hb >> (t / BS)) & 1u);
-            x[t] = see ? x[t] : -INFINITY;
+          for (int u = 0; u < 32; ++u) {
+            float v0, v1;
+            unpair2(x[u], v0, v1);
+            const bool see0 = (unsigned)(2 * u - a) < len && ((hb >> (2 * u / BS)) & 1u);
+            const bool see1 = (unsigned)(2 * u + 1 - a) < len && ((hb >> (2 * u / BS)) & 1u);
+            x[u] = pair2(see0 ? v0 : -INFINITY, see1 ? v1 : -INFINITY);
           }
         }
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int t = 0; t < 64; ++t) mq[t & 3] = fmaxf(mq[t & 3], x[t]);
-        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * mul;
+        const float mx = max64(x) * mul;
         const bool move = mx > m_ref + 8.f;
         const bool resc = move && m_ref != -INFINITY;  // O's row holds terms to rescale
         const float f = resc ? fast_exp2(m_ref - mx) : 1.f;
@@ -417,14 +531,21 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         // result by at most the rounding unit times the row's largest |v|. A row that has seen nothing yet
         // exponentiates against 0 (its x are -inf, or NaN, which must stay).
         uint32_t pw[32];
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        f32x2 ls[4] = {0ull, 0ull, 0ull, 0ull};
         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+        const f32x2 mul2v = pair2(mul, mul), nm2 = pair2(nm, nm);
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
-          const float p0 = fast_exp2(fmaf(x[2 * u], mul, nm)), p1 = fast_exp2(fmaf(x[2 * u + 1], mul, nm));
-          pw[u] = Elem<TP>::pack2(p0, p1);
-          ls[u & 3] += p0 + p1;
+          float a, b;
+          unpair2(fma2(x[u], mul2v, nm2), a, b);
+          a = fast_exp2(a);
+          b = fast_exp2(b);
+          pw[u] = Elem<TP>::pack2(a, b);
+          ls[u & 3] = add2(ls[u & 3], pair2(a, b));
         }
+        float lsum, lodd;
+        unpair2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), lsum, lodd);
+        lsum += lodd;
         if (__any_sync(kFull, resc)) {  // the whole warp moves its rows' O (factor 1 for rows that keep theirs)
           // the tile before is done (its P's columns hold this S); the half before may still be multiplied
           if (hf > 0) ok = __all_sync(kFull, tc_wait(pv_half + w, n & 1, abort));
@@ -440,7 +561,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             tc::st32(ocol + c * 32, o);
           }
         }
-        l = l * f + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+        l = l * f + lsum;
         tc::st32(scol + hf * 64, pw);  // P over S
         tc::wait_st();
         // V rows that were not copied, or lie outside the CTA's keys, may hold anything (NaN): zero them once
