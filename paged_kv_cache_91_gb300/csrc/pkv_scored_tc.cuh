@@ -19,11 +19,16 @@
 // overlap the two, and a score is kept to few instructions: tiles that every row sees whole skip the masks,
 // and the tanh is a polynomial where the tile's scores stay well below the cap.
 //
+// A CTA stays and takes one (partition, row tile, kv head, sequence) after the other: when its copies of an item
+// are issued it asks the hardware for the next unstarted CTA of the grid and does that one's work too. So the
+// copies and first products of an item run under the end of the one before, and tensor memory and barriers are
+// set up once.
+//
 // Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 and 11 copy the
 // blocks of K and V tiles, half of each tile a warp (a copy takes about 100 cycles to issue), into a ring of
-// tile slots in the order K0 V0 K1 V1 ...; FP8 pool: 12-15 widen a tile's codes to f16 in place.
-// Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set PKV_DEVERR_TIMEOUT and
-// write zeros.
+// tile slots in the order K0 V0 K1 V1 ..., and 10 finds the items; FP8 pool: 12-15 widen a tile's codes to f16
+// in place. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set
+// PKV_DEVERR_TIMEOUT and write zeros for the item's rows.
 #pragma once
 
 #include <type_traits>
@@ -63,6 +68,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // The largest of 64 values held as pairs, and of their negatives (four chains of three-way maxima).
 __device__ __forceinline__ float max64(const f32x2 (&x)[32]) {
   float m[4], a, b;
@@ -83,19 +93,25 @@ __device__ __forceinline__ float max64neg(const f32x2 (&x)[32]) {
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
-// The 64 weights 2^e(u) (pairs) in 16 bits into pw; returns the sum of the fp32 weights before that rounding,
-// which moves the result by at most the rounding unit times the row's largest |v|.
+// The 64 weights 2^e(u) (pairs) in 16 bits into the tensor-memory columns from pcol on, half of them at a time (the
+// registers); returns the sum of the fp32 weights before that rounding, which moves the result by at most the
+// rounding unit times the row's largest |v|.
 template <typename TP, typename E>
-__device__ __forceinline__ float weights64(uint32_t (&pw)[32], E e) {
+__device__ __forceinline__ float weights64(uint32_t pcol, E e) {
   f32x2 ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int u = 0; u < 32; ++u) {
-    float a, b;
-    unpair2(e(u), a, b);
-    a = fast_exp2(a);
-    b = fast_exp2(b);
-    pw[u] = Elem<TP>::pack2(a, b);
-    ls[u & 3] = add2(ls[u & 3], pair2(a, b));
+  for (int i = 0; i < 2; ++i) {
+    uint32_t pw[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      float a, b;
+      unpair2(e(16 * i + u), a, b);
+      a = fast_exp2(a);
+      b = fast_exp2(b);
+      pw[u] = Elem<TP>::pack2(a, b);
+      ls[u & 3] = add2(ls[u & 3], pair2(a, b));
+    }
+    tc::st16(pcol + 16 * i, pw);
   }
   float a, b;
   unpair2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), a, b);
@@ -115,10 +131,13 @@ struct ScoredTcShape {
   static constexpr int HALF = TILE / 2;      // FP8 pool: a tile's codes land in its slot's upper half
   static constexpr int OFF_RING = 2 * QT;
   static constexpr int OFF_BARS = OFF_RING + NS * TILE;
-  // barriers: full[8], empty[8], raw[8] per slot; per stream q_full, fin; per stream and half s_full, p_full, pv_done
-  static constexpr int NBARS = 24 + 16;
-  static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;  // tensor-memory base, abort flag, key range, row state
-  static constexpr int OFF_ML = OFF_MISC + 16;           // stream 1's (m, l) in a CTA of shared rows
+  // barriers: full[8], empty[8], raw[8] per slot; per stream q_full, fin; per stream and half s_full, p_full,
+  // pv_done; items: info_full[2], info_empty[2], next
+  static constexpr int NBARS = 24 + 16 + 5;
+  static constexpr int OFF_NEXT = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;  // the hardware's answer: the next CTA
+  static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag
+  static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
+  static constexpr int OFF_ML = OFF_INFO + 2 * 64;                       // stream 1's (m, l) in an item of shared rows
   static constexpr int SMEM = OFF_ML + 2 * ROWS * 4;
   static constexpr int S_COL = 0, O_COL = 256;  // tensor memory: stream w's S at 128 w, its O at 256 + 128 w
   static constexpr int TMEM_COLS = 512;
@@ -127,7 +146,6 @@ struct ScoredTcShape {
   static_assert(SMEM <= 232448 - 1024, "one CTA's shared memory");
   static_assert(NBT >= 4 && NBT <= 16, "blocks per tile");
   static_assert(!F8 || D == 128, "an FP8 pool: head_dim 128");
-  static_assert(2 * ROWS * D * 2 <= NS * TILE, "the merge of the streams stages one O in the ring");
 };
 
 // Whether every thread of the four widening warps says yes.
@@ -142,6 +160,33 @@ __device__ __forceinline__ bool widen_agree(bool yes) {
       : "r"(yes ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+
+// The n lowest bits (all from 32 on, none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Each lane of a quad holds four 16-byte units u[0..3] of its row; afterwards lane q holds unit q of the quad's
+// rows 0..3, so that the quad stores 64 consecutive bytes of one row at a time.
+__device__ __forceinline__ void quad_transpose(uint32_t (&u)[16], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // units i and i + d
+        uint32_t &a = u[4 * i + e], &b = u[4 * (i + d) + e];
+        const uint32_t got = __shfl_xor_sync(kFull, up ? a : b, d);
+        if (up)
+          a = got;
+        else
+          b = got;
+      }
+    }
+  }
 }
 
 // x -= slope |d0 - t| for the half's 64 keys t.
@@ -188,6 +233,176 @@ __device__ __forceinline__ void scored_widen(unsigned char* slot, int half, int 
   }
 }
 
+// One CTA's work of the grid: the rows of a row tile and their keys [c0, c1).
+struct ScoredItem {
+  int ntile;  // tiles; 0: no key (rows that see nothing may need their zeros); -1: no more items
+  int part, rt, kvh, s;
+  int ctx, q0, q_len;
+  int c0, c1;
+  __device__ __forceinline__ long long row0() const { return (long long)rt * 256; }
+  __device__ __forceinline__ int nrows(int G) const { return (int)min(256ll, (long long)q_len * G - row0()); }
+};
+
+// The item of CTA (x, y, z) of the grid, on one warp. ntile = -2: nothing to do.
+template <int BS, int NT>
+__device__ __forceinline__ ScoredItem scored_item(const DecodeParams& p, const ScoreParams& sc, int x, int y, int z,
+                                                  int lane) {
+  ScoredItem m;
+  m.ntile = -2;
+  // the last row tiles first: with a causal limit they see the most keys
+  m.part = x / sc.row_tiles;
+  m.rt = sc.row_tiles - 1 - x % sc.row_tiles;
+  m.kvh = y;
+  m.s = sc.order ? sc.order[z] : z;
+  const bool reporter = x == 0 && y == 0 && lane == 0;
+  m.ctx = clamp_context(p, m.s, reporter);
+  m.q0 = 0;
+  m.q_len = scored_query_len(sc, m.s, m.ctx, m.q0);
+  if (m.q_len < 0) {
+    if (reporter) atomicOr(p.err, PKV_DEVERR_QUERY);
+    return m;
+  }
+  const int G = p.group;
+  if (m.row0() >= (long long)m.q_len * G) return m;
+  // its rows' first and last visible key, within the partition
+  const int ta = (int)(m.row0() / G), tb = (int)((m.row0() + m.nrows(G) - 1) / G);
+  const int p0 = m.ctx - m.q_len;  // position of the sequence's first query token
+  int a = INT32_MAX, b = 0;
+  if (!sc.key_begin && !sc.key_end) {  // the first token's first, the last token's last
+    int unused;
+    scored_span(sc, 0, p0 + ta, m.ctx, a, unused);
+    scored_span(sc, 0, p0 + tb, m.ctx, unused, b);
+  } else {
+    for (int t = ta + lane; t <= tb; t += 32) {
+      int lo, hi;
+      scored_span(sc, m.q0 + t, p0 + t, m.ctx, lo, hi);
+      if (hi > lo) {
+        a = min(a, lo);
+        b = max(b, hi);
+      }
+    }
+    a = __reduce_min_sync(kFull, a);
+    b = __reduce_max_sync(kFull, b);
+  }
+  const int tok0 = scored_base(sc, m.ctx, m.q_len, BS) + m.part * p.partition_size;
+  m.c0 = max(a, tok0);
+  m.c1 = min(b, tok0 + p.partition_size);
+  if (m.c1 <= m.c0)
+    m.ntile = m.part == 0 ? 0 : -2;
+  else
+    m.ntile = (m.c1 - m.c0 / BS * BS + NT - 1) / NT;
+  return m;
+}
+
+// Ask for the next unstarted CTA of the grid; the answer lands at `dst` (16 bytes) and completes `bar`.
+__device__ __forceinline__ void ask_next_cta(void* dst, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(dst)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The answer: false if there is none left, else its index.
+__device__ __forceinline__ bool next_cta(const void* src, int& x, int& y, int& z) {
+  uint32_t got, a, b, c;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
+      : "=r"(got), "=r"(a), "=r"(b), "=r"(c)
+      : "r"(smem_u32(src))
+      : "memory");
+  x = (int)a;
+  y = (int)b;
+  z = (int)c;
+  return got != 0;
+}
+
+// A stream's warp brings its 32 query rows into Q's A-operand layout (128-byte swizzled rows, columns 64.. in the
+// next ROWS x 128 bytes), asynchronously, a row's bytes by neighbouring lanes. Lane l's own row is row l: its
+// index in query, or -1 for zeros.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void scored_fetch_q(unsigned char* Qs, int wq, int lane, const T* query, int own) {
+  constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows per instruction
+  const int c = lane % CH;
+#pragma unroll
+  for (int i = 0; i < 32 / RPI; ++i) {
+    const int rl = i * RPI + lane / CH;
+    const int idx = __shfl_sync(kFull, own, rl);
+    const int r = 32 * wq + rl;
+    cp_async16(smem_u32(Qs) + r * 128 + (c / 8) * (ROWS * 128) + (((c % 8) ^ (r & 7)) << 4),
+               query + (idx < 0 ? 0 : (size_t)idx * D) + c * 8, idx < 0 ? 0u : 16u);
+  }
+}
+
+// FP8 pool with a bf16 query: the same rows in f16, each multiplied by 2^k so that its largest magnitude lies in
+// [2^14, 2^15) (every bf16 value keeps its 8 significant bits unless it lies below 2^-14 of that range, where its
+// contribution is far below the fp32 accumulation error). Returns this lane's row's 2^-k. store: write them.
+template <int ROWS>
+__device__ __forceinline__ float scored_fetch_q_bf16_as_f16(unsigned char* Qs, int wq, int lane,
+                                                            const __nv_bfloat16* query, int own, bool store) {
+  constexpr int D = 128;
+  const int c = lane & 15;
+  float mine = 1.f;
+  uint4 rows[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int idx = __shfl_sync(kFull, own, 2 * i + (lane >> 4));
+    rows[i] = make_uint4(0, 0, 0, 0);
+    if (idx >= 0) rows[i] = *reinterpret_cast<const uint4*>(query + (size_t)idx * D + c * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int rl = 2 * i + (lane >> 4);
+    const uint4 v = rows[i];
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = Elem<__nv_bfloat16>::to_float2(w[e]);
+      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;  // floor(log2(amax))
+    int k = amax > 0.f ? 14 - ex : 0;
+    k = k < -60 ? -60 : (k > 60 ? 60 : k);
+    const float pw = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    const float i0 = __shfl_sync(kFull, inv, 0), i1 = __shfl_sync(kFull, inv, 16);
+    if (lane == 2 * i) mine = i0;
+    if (lane == 2 * i + 1) mine = i1;
+    if (store) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Elem<__nv_bfloat16>::to_float2(w[e]);
+        w[e] = Elem<__half>::pack2(f.x * pw, f.y * pw);
+      }
+      const int r = 32 * wq + rl;
+      *reinterpret_cast<uint4*>(Qs + r * 128 + (c / 8) * (ROWS * 128) + (((c % 8) ^ (r & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  return mine;
+}
+
+// Whether every thread of the two streams' rows says yes.
+__device__ __forceinline__ bool rows_agree(bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(yes ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 template <typename T, int D, int BS, bool F8, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     pkv_scored_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ ScoreParams sc,
@@ -205,93 +420,26 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   uint64_t* s_full = bars + 28;   // [stream][half]
   uint64_t* p_full = bars + 32;   // [stream][half]
   uint64_t* pv_done = bars + 36;  // [stream][half]
+  uint64_t* info_full = bars + 40;   // [2]
+  uint64_t* info_empty = bars + 42;  // [2]
+  uint64_t* next_bar = bars + 44;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* range = reinterpret_cast<int*>(tmem_slot + 2);  // first visible key, end of the visible keys
+  static_assert(sizeof(ScoredItem) <= 64, "an item's place");
+  auto info = [&](int k) { return reinterpret_cast<ScoredItem*>(smem + Sh::OFF_INFO + (k & 1) * 64); };
   auto slot = [&](int it) { return smem + Sh::OFF_RING + (it % NS) * Sh::TILE; };
-
-  // the last row tiles first: with a causal limit they see the most keys
-  const int part = blockIdx.x / sc.row_tiles, rt = sc.row_tiles - 1 - (int)blockIdx.x % sc.row_tiles;
-  const int kvh = blockIdx.y;
-  const int s = sc.order ? sc.order[blockIdx.z] : (int)blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, P = p.partition_size;
-  const bool reporter = blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0;
   if (smem_u32(smem) & 1023u) {  // not expected on any supported GPU; nothing is written
     if (threadIdx.x == 0) atomicOr(p.err, PKV_DEVERR_LAYOUT);
     return;
   }
-  const int ctx = clamp_context(p, s, reporter);
-  int q0 = 0;
-  const int q_len = scored_query_len(sc, s, ctx, q0);
-  if (q_len < 0) {
-    if (reporter) atomicOr(p.err, PKV_DEVERR_QUERY);
-    return;
-  }
-  const long long R = (long long)q_len * G, row0 = (long long)rt * 2 * ROWS;
-  if (row0 >= R) return;
-  const int nrows = (int)min((long long)2 * ROWS, R - row0);
-  const bool shared_rows = nrows <= ROWS;  // both streams take the same rows
-  const int base = scored_base(sc, ctx, q_len, BS);
-  const int tok0 = base + part * P;
-
-  // the streams' rows: warps 0-7, thread row = its tensor-memory lane
-  const int w = warp >> 2;  // (stream, for warps 0-7)
-  const int row = 32 * (warp & 3) + lane;
-  const int rr = (shared_rows ? 0 : w * ROWS) + row;  // row within the CTA
-  const bool active = warp < 8 && rr < nrows;
-  const int ti = active ? (int)((row0 + rr) / G) : 0;  // query token within the sequence
-  const int h = kvh * G + (active ? (int)((row0 + rr) % G) : 0);
-  const int pos = ctx - q_len + ti;
-  int lo = 0, hi = 0;
-  if (active) scored_span(sc, q0 + ti, pos, ctx, lo, hi);
-  const RowParts parts = row_parts(lo, hi, base, P);
-
-  // the CTA's keys: from its rows' first to their last visible one, within the partition
-  int c0, c1;
-  if (!sc.key_begin && !sc.key_end) {  // the first row's first, the last row's last
-    int unused;
-    scored_span(sc, 0, ctx - q_len + (int)(row0 / G), ctx, c0, unused);
-    scored_span(sc, 0, ctx - q_len + (int)((row0 + nrows - 1) / G), ctx, unused, c1);
-  } else {
-    if (threadIdx.x == 0) {
-      range[0] = INT32_MAX;
-      range[1] = 0;
-    }
-    __syncthreads();
-    if (warp < 8) {
-      int a = hi > lo ? lo : INT32_MAX, b = hi > lo ? hi : 0;
-      a = __reduce_min_sync(kFull, a);
-      b = __reduce_max_sync(kFull, b);
-      if (lane == 0) {
-        atomicMin(range, a);
-        atomicMax(range + 1, b);
-      }
-    }
-    __syncthreads();
-    c0 = range[0];
-    c1 = range[1];
-  }
-  c0 = max(c0, tok0);
-  c1 = min(c1, tok0 + P);
-  T* out_row = static_cast<T*>(p.out) + ((size_t)(q0 + ti) * p.num_heads + h) * D;
-  if (c1 <= c0) {  // no key: partition 0 writes the zeros of rows that see nothing
-    if (part == 0 && active && parts.last < parts.first)
-      for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out_row + d) = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const int blk0 = c0 / BS, nblk = (c1 + BS - 1) / BS - blk0;
-  const int ntile = (nblk + NBT - 1) / NBT;
-  const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq + blk0;
-  const int step = shared_rows ? 2 : 1;                  // a stream's tiles: first, first + step, ...
-  auto first_tile = [&](int stream) { return shared_rows ? stream : 0; };
-
   if (threadIdx.x == 0) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + k, F8 ? 4 : 2);
-      mbar_init(empty + k, shared_rows ? 1 : 2);
+      mbar_init(empty + k, 2);
       mbar_init(raw + k, 2);
     }
     for (int k = 0; k < 2; ++k) {
@@ -302,7 +450,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         mbar_init(p_full + 2 * k + hf, ROWS);
         mbar_init(pv_done + 2 * k + hf, 1);
       }
+      mbar_init(info_full + k, 1);
+      mbar_init(info_empty + k, Sh::THREADS / 32 - 1);  // every warp but the one that finds the items
     }
+    mbar_init(next_bar, 1);
     fence_mbar_init();
     *abort = 0;
   }
@@ -312,391 +463,572 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   tc::fence_after_sync();
   const uint32_t tbase = *tmem_slot;
 
+  // Item k, read by a whole warp; its place is then free again. False: none came in time.
+  auto wait_item = [&](int k) { return __all_sync(kFull, tc_wait(info_full + (k & 1), (k >> 1) & 1, abort)) != 0; };
+  auto free_item = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(info_empty + (k & 1));
+  };
+  auto read_item = [&](int k, ScoredItem& m) {
+    if (!wait_item(k)) return false;
+    m = *info(k);
+    free_item(k);
+    return true;
+  };
+  // A stream's tiles of an item: first, first + step, ...; shared: both streams take the same rows.
+  auto shared_rows = [&](const ScoredItem& m) { return m.nrows(G) <= ROWS; };
+
   if (warp == Sh::COPY_WARP || warp == Sh::COPY_WARP + 1) {
-    // ---- copies: this warp's half of the blocks of item it = 2 j (K tile j) and 2 j + 1 (V tile j)
+    // ---- copies: this warp's half of the blocks of the ring's items it = 2 j (K tile j) and 2 j + 1 (V tile j)
     constexpr int NH = NBT / 2;
     const int at = (warp - Sh::COPY_WARP) * NH + (lane & (NH - 1));  // lane < NH: block of the tile
     uint64_t* landed = F8 ? raw : full;
-    auto load_id = [&](int j) { return lane < NH && j * NBT + at < nblk ? table[j * NBT + at] : -1; };
-    int next = load_id(0);
-    int it = 0;
+    const bool finder = warp == Sh::COPY_WARP;
+    ScoredItem m;
+    int k = 0, it = 0, asked = 0;
     bool ok = true;
-    for (int j = 0; ok && j < ntile; ++j) {
-      int id = next;
-      if (j + 1 < ntile) next = load_id(j + 1);
-      if (lane < NH && j * NBT + at < nblk && (unsigned)id >= (unsigned)p.num_blocks) {
-        atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
-        id = -1;
+    // The finder's next item with anything to do, published; x, y, z: the first CTA to look at, or have = false.
+    auto find = [&](bool have, int x, int y, int z) {
+      m.ntile = -2;
+      while (ok && m.ntile == -2) {
+        if (!have) {
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the answer before has been read
+            ask_next_cta(smem + Sh::OFF_NEXT, next_bar);
+          }
+          __syncwarp();
+          ok = __all_sync(kFull, tc_wait(next_bar, asked & 1, abort));
+          ++asked;
+          if (!ok) {  // the answer may not land in a CTA that has left
+            mbar_wait(next_bar, (asked - 1) & 1);
+            break;
+          }
+          have = next_cta(smem + Sh::OFF_NEXT, x, y, z);
+          __syncwarp();
+        }
+        if (have)
+          m = scored_item<BS, NT>(p, sc, x, y, z, lane);
+        else
+          m.ntile = -1;  // (nothing is asked again)
+        have = false;
       }
-      const int n = __popc(__ballot_sync(kFull, id >= 0));
-      const int y = (id * p.num_kv_heads + kvh) * BS;  // first pool row of the block
+      if (ok && k >= 2) ok = __all_sync(kFull, tc_wait(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
+      if (!ok) return;
+      if (lane == 0) {
+        *info(k) = m;
+        mbar_arrive(info_full + (k & 1));
+      }
+      __syncwarp();
+    };
+    if (finder)
+      find(true, blockIdx.x, blockIdx.y, blockIdx.z);
+    else
+      ok = read_item(0, m);
+    while (ok && m.ntile >= 0) {
+      const int blk0 = m.c0 / BS, nblk = m.ntile > 0 ? (m.c1 + BS - 1) / BS - blk0 : 0;
+      const int32_t* table = p.block_tables + (size_t)m.s * p.max_blocks_per_seq + blk0;
+      auto load_id = [&](int j) { return lane < NH && j * NBT + at < nblk ? table[j * NBT + at] : -1; };
+      int next = load_id(0);
+      for (int j = 0; ok && j < m.ntile; ++j) {
+        int id = next;
+        if (j + 1 < m.ntile) next = load_id(j + 1);
+        if (lane < NH && j * NBT + at < nblk && (unsigned)id >= (unsigned)p.num_blocks) {
+          atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+          id = -1;
+        }
+        const int n = __popc(__ballot_sync(kFull, id >= 0));
+        const int y = (id * p.num_kv_heads + m.kvh) * BS;  // first pool row of the block
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++it) {
-        uint64_t* bar = landed + it % NS;
-        if (it >= NS) ok = __all_sync(kFull, tc_wait(empty + it % NS, (it / NS - 1) & 1, abort));
-        if (!ok) break;
-        if (lane == 0) {
-          fence_proxy_async_smem();  // generic stores into the slot (zeroed rows, widened codes): before the copies
-          mbar_arrive_expect_tx(bar, n * BS * (F8 ? 128 : D * 2));
-        }
-        __syncwarp();
-        if (id >= 0) {
-          if constexpr (F8)
-            tma_load_2d(slot(it) + Sh::HALF + at * BS * 128, kv ? &vmap : &kmap, 0, y, bar);
-          else if constexpr (Sh::DH == 2)
-            tma_load_4d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, 0, 0, y / 8, bar);
-          else
-            tma_load_2d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, y, bar);
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          uint64_t* bar = landed + it % NS;
+          if (it >= NS) ok = __all_sync(kFull, tc_wait(empty + it % NS, (it / NS - 1) & 1, abort));
+          if (!ok) break;
+          if (lane == 0) {
+            fence_proxy_async_smem();  // generic stores into the slot (zeroed rows, widened codes): before the copies
+            mbar_arrive_expect_tx(bar, n * BS * (F8 ? 128 : D * 2));
+          }
+          __syncwarp();
+          if (id >= 0) {
+            if constexpr (F8)
+              tma_load_2d(slot(it) + Sh::HALF + at * BS * 128, kv ? &vmap : &kmap, 0, y, bar);
+            else if constexpr (Sh::DH == 2)
+              tma_load_4d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, 0, 0, y / 8, bar);
+            else
+              tma_load_2d(slot(it) + at * (BS / 8) * Sh::ATOM, kv ? &vmap : &kmap, 0, y, bar);
+          }
         }
       }
+      ++k;
+      if (!ok) break;
+      if (finder)
+        find(false, 0, 0, 0);
+      else
+        ok = read_item(k, m);
     }
     // no copy may still be landing when the CTA leaves
     if (lane == 0)
-      for (int k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait(landed + k % NS, (k / NS) & 1);
+      for (int i = it > NS ? it - NS : 0; i < it; ++i) mbar_wait(landed + i % NS, (i / NS) & 1);
   } else if (F8 && warp >= Sh::WIDEN_WARP) {
-    // ---- FP8 pool: widen each item's codes once they have landed
-    for (int it = 0; it < 2 * ntile; ++it) {
-      // (agreed among the four warps, which meet at barriers: all go on, or all leave)
-      if (!widen_agree(tc_wait(raw + it % NS, (it / NS) & 1, abort))) break;
-      if constexpr (F8) scored_widen(slot(it), Sh::HALF, warp - Sh::WIDEN_WARP, lane);
-      fence_proxy_async_smem();  // generic stores, read by the MMAs
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + it % NS);
+    // ---- FP8 pool: widen each slot's codes once they have landed
+    // (agreed among the four warps, which meet at barriers: all go on, or all leave)
+    ScoredItem m;
+    int it = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      ok = widen_agree(read_item(k, m));
+      if (!ok || m.ntile < 0) break;
+      for (int i = 0; i < 2 * m.ntile; ++i, ++it) {
+        ok = widen_agree(tc_wait(raw + it % NS, (it / NS) & 1, abort));
+        if (!ok) break;
+        if constexpr (F8) scored_widen(slot(it), Sh::HALF, warp - Sh::WIDEN_WARP, lane);
+        fence_proxy_async_smem();  // generic stores, read by the MMAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + it % NS);
+      }
     }
   } else if (warp == Sh::MMA_WARP || warp == Sh::MMA_WARP + 1) {
     // ---- MMA issue: one thread per stream, in the order S S | PV S | PV S | ... by halves of a tile
-    if (lane == 0) {
-      const int st = warp - Sh::MMA_WARP;
-      constexpr bool BF = std::is_same<TP, __nv_bfloat16>::value;
-      constexpr uint32_t IDESC_S = tc::idesc_f16(BF, ROWS, NT / 2, false, false);
-      constexpr uint32_t IDESC_O = tc::idesc_f16(BF, ROWS, D, false, true);
-      const uint32_t q_addr = smem_u32(smem) + (shared_rows ? 0 : st * Sh::QT);
-      const uint32_t scol = tbase + Sh::S_COL + st * NT, ocol = tbase + Sh::O_COL + st * 128;
-      // S of tile j's half hf (64 keys: 8 atoms of K) into that half's columns, which the caller knows are free
-      auto issue_s = [&](int j, int hf) {
-        const int ik = 2 * j;
-        if (hf == 0 && !tc_wait(full + ik % NS, (ik / NS) & 1, abort)) return false;
-        tc::fence_after_sync();
-        const uint32_t k_addr = smem_u32(slot(ik)) + hf * 8 * Sh::ATOM;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_f16(scol + hf * 64, tc::desc_sw128(q_addr + (k / 4) * (ROWS * 128) + (k % 4) * 32, 16, 1024),
-                      tc::desc_sw128(k_addr + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::ATOM), IDESC_S, k > 0);
-        tc::commit(s_full + 2 * st + hf);
-        if (hf) tc::commit(empty + ik % NS);
-        return true;
-      };
-      bool ok = shared_rows ? tc_wait(q_full, 0, abort) && tc_wait(q_full + 1, 0, abort) : tc_wait(q_full + st, 0, abort);
-      int j = first_tile(st), n = 0;
-      if (j < ntile) ok = ok && issue_s(j, 0) && issue_s(j, 1);
-      for (; ok && j < ntile; j += step, ++n) {
-        const int iv = 2 * j + 1;
-        const uint32_t v_addr = smem_u32(slot(iv));
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          ok = ok && tc_wait(p_full + 2 * st + hf, n & 1, abort) &&
-               (hf > 0 || tc_wait(full + iv % NS, (iv / NS) & 1, abort));
-          if (!ok) break;
+    const int st = warp - Sh::MMA_WARP;
+    constexpr bool BF = std::is_same<TP, __nv_bfloat16>::value;
+    constexpr uint32_t IDESC_S = tc::idesc_f16(BF, ROWS, NT / 2, false, false);
+    constexpr uint32_t IDESC_O = tc::idesc_f16(BF, ROWS, D, false, true);
+    const uint32_t scol = tbase + Sh::S_COL + st * NT, ocol = tbase + Sh::O_COL + st * 128;
+    ScoredItem m;
+    int tiles = 0, cnt = 0, nq = 0;  // ring tiles of the items before, this stream's tiles, items with keys
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      ok = read_item(k, m);
+      if (!ok || m.ntile < 0) break;
+      if (m.ntile == 0) continue;
+      const bool shared = shared_rows(m);
+      const int first = shared ? st : 0, step = shared ? 2 : 1;
+      if (lane == 0 && first < m.ntile) {
+        const uint32_t q_addr = smem_u32(smem) + (shared ? 0 : st * Sh::QT);
+        // S of tile j's half hf (64 keys: 8 atoms of K) into that half's columns, which the caller knows are free
+        auto issue_s = [&](int j, int hf) {
+          const int ik = 2 * (tiles + j);
+          if (hf == 0 && !tc_wait(full + ik % NS, (ik / NS) & 1, abort)) return false;
           tc::fence_after_sync();
+          const uint32_t k_addr = smem_u32(slot(ik)) + hf * 8 * Sh::ATOM;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 16 keys each: 8 columns of P, two atoms of V
-            tc::mma_f16_ta(ocol, scol + hf * 64 + k * 8,
-                           tc::desc_sw128(v_addr + (hf * 4 + k) * 2 * Sh::ATOM, 1024, Sh::ATOM), IDESC_O,
-                           n > 0 || hf > 0 || k > 0);
-          tc::commit(pv_done + 2 * st + hf);
-          if (hf) tc::commit(empty + iv % NS);
-          // the next tile's S goes where this half's P is: not before its PV has read it
-          if (j + step < ntile) ok = tc_wait(pv_done + 2 * st + hf, n & 1, abort) && issue_s(j + step, hf);
+          for (int u = 0; u < D / 16; ++u)
+            tc::mma_f16(scol + hf * 64, tc::desc_sw128(q_addr + (u / 4) * (ROWS * 128) + (u % 4) * 32, 16, 1024),
+                        tc::desc_sw128(k_addr + (u / 4) * 1024 + (u % 4) * 32, 16, Sh::ATOM), IDESC_S, u > 0);
+          tc::commit(s_full + 2 * st + hf);
+          if (hf) {
+            tc::commit(empty + ik % NS);
+            if (shared) tc::commit(empty + ik % NS);  // (the other stream does not read this tile)
+          }
+          return true;
+        };
+        // a P's columns take the next S: not before its PV has read it
+        auto pv_read = [&](int hf) { return cnt == 0 || tc_wait(pv_done + 2 * st + hf, (cnt - 1) & 1, abort); };
+        ok = tc_wait(q_full + st, nq & 1, abort) && (!shared || tc_wait(q_full + (st ^ 1), nq & 1, abort));
+        ok = ok && pv_read(0) && issue_s(first, 0) && pv_read(1) && issue_s(first, 1);
+        for (int j = first; ok && j < m.ntile; j += step) {
+          const int iv = 2 * (tiles + j) + 1;
+          const uint32_t v_addr = smem_u32(slot(iv));
+          ++cnt;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            ok = ok && tc_wait(p_full + 2 * st + hf, (cnt - 1) & 1, abort) &&
+                 (hf > 0 || tc_wait(full + iv % NS, (iv / NS) & 1, abort));
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int u = 0; u < 4; ++u)  // 16 keys each: 8 columns of P, two atoms of V
+              tc::mma_f16_ta(ocol, scol + hf * 64 + u * 8,
+                             tc::desc_sw128(v_addr + (hf * 4 + u) * 2 * Sh::ATOM, 1024, Sh::ATOM), IDESC_O,
+                             j > first || hf > 0 || u > 0);
+            tc::commit(pv_done + 2 * st + hf);
+            if (hf) {
+              tc::commit(empty + iv % NS);
+              if (shared) tc::commit(empty + iv % NS);
+            }
+            if (j + step < m.ntile) ok = pv_read(hf) && issue_s(j + step, hf);
+          }
         }
       }
+      tiles += m.ntile;
+      ++nq;
+      ok = __all_sync(kFull, ok);
+    }
+    if (lane == 0) {
       tc::commit(fin + st);  // every MMA issued above has completed once this arrives
       mbar_wait(fin + st, 0);
     }
     __syncwarp();
   } else if (warp < 8) {
     // ---- rows
-    float qscale = 1.f;  // FP8 pool, bf16 query: the 2^-k the row was scaled by
-    unsigned char* Qs = smem + (shared_rows ? 0 : w * Sh::QT);
-    // (row tile rt of 256 rows: stream w's rows are tile 2 rt + w of 128 rows)
-    const int rt128 = 2 * rt + (shared_rows ? 0 : w);
-    if constexpr (F8 && std::is_same<T, __nv_bfloat16>::value) {
-      // (in a CTA of shared rows both streams need the factor; both store the same Q)
-      qscale = mq_tc_fetch_q_bf16_as_f16<D, ROWS>(Qs, row, reinterpret_cast<const __nv_bfloat16*>(p.query), q0, kvh,
-                                                  rt128, q_len, G, p.num_heads);
-    } else if (!shared_rows || w == 0) {
-      mq_tc_fetch_q<T, D, ROWS>(Qs, row, reinterpret_cast<const T*>(p.query), q0, kvh, rt128, q_len, G, p.num_heads);
-      cp_async_wait_all();
-    }
-    fence_proxy_async_smem();  // generic-proxy writes, read by the S MMAs
-    mbar_arrive(q_full + w);
-    const float sl2 = p.scale_log2 * qscale;
-    const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
-    const float slope = BIAS ? sc.slopes[h] * 1.4426950408889634f : 0.f;
-    // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
-    // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers leave fp32's range.)
-    f32x2 cc[4];
-    float near2 = -1.f;  // the largest x^2 that it is for
-    {
-      const float z2 = cap_in * cap_in;
-      float c = cap_out * cap_in;
-      const float fit[4] = {0.999999456f, -0.333263179f, 0.131902965f, -0.0444022226f};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        cc[k] = pair2(c * fit[k], c * fit[k]);
-        c *= z2;
-      }
-      if (z2 < 1e6f && z2 > 1e-18f) near2 = 0.25f / z2;
-    }
-    const int t_first = blk0 * BS;
+    const int w = warp >> 2;                  // stream
+    const int row = 32 * (warp & 3) + lane;   // row of the stream: its tensor-memory lane
     const uint32_t scol = tc::taddr(tbase, 32 * (warp & 3), Sh::S_COL + w * NT);
     const uint32_t ocol = tc::taddr(tbase, 32 * (warp & 3), Sh::O_COL + w * 128);
-    // which blocks of a tile were copied: lane b < NBT holds block b's test (the copying warps' own)
-    auto load_ok = [&](int j) {
-      const int b = j * NBT + (lane & (NBT - 1));
-      return b < nblk ? (unsigned)table[b] < (unsigned)p.num_blocks : false;
+    float* ml = reinterpret_cast<float*>(smem + Sh::OFF_ML);
+    constexpr bool Q_AS_F16 = F8 && std::is_same<T, __nv_bfloat16>::value;
+    // (an item is read where it lies, and its place freed at its end: the row loop has no registers to spare)
+    int tiles = 0, cnt = 0;  // ring tiles of the items before, this stream's tiles
+    float qscale = 1.f, qscale_next = 1.f;  // FP8 pool, bf16 query: the 2^-k the row was scaled by
+    // this thread's row of an item, as an index into the output's rows; -1: none
+    auto own_row = [&](const ScoredItem& i, int& ti, int& h) {
+      const int rr = (shared_rows(i) ? 0 : w * ROWS) + row;
+      if (rr >= i.nrows(G)) {
+        ti = 0;
+        h = i.kvh * G;
+        return -1;
+      }
+      const long long r = i.row0() + rr;
+      ti = (int)(r / G);
+      h = i.kvh * G + (int)(r - (long long)ti * G);
+      return (i.q0 + ti) * p.num_heads + h;
     };
-    constexpr uint32_t all = NBT == 32 ? 0xffffffffu : (1u << NBT) - 1u;
-    float m_ref = -INFINITY, l = 0.f;
-    bool ok = true;
-    int n = 0;
-    bool next = first_tile(w) < ntile && load_ok(first_tile(w));
-    for (int j = first_tile(w); j < ntile; j += step, ++n) {
-      const uint32_t blocks = __ballot_sync(kFull, next) & all;
-      if (j + step < ntile) next = load_ok(j + step);
-      const int tb = t_first + j * NT;  // position of the tile's first token
-      const bool edge = blocks != all || tb < c0 || tb + NT > c1;  // V rows outside the CTA's keys, or not copied
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        const int th = tb + hf * 64;
-        // (tensor-memory accesses are warp-wide: a warp leaves the loop as a whole)
-        ok = __all_sync(kFull, tc_wait(s_full + 2 * w + hf, n & 1, abort));
-        if (!ok) break;
-        tc::fence_after_sync();
-        uint32_t sr[2][32];
-        tc::ld32(scol + hf * 64, sr[0]);
-        tc::ld32(scol + hf * 64 + 32, sr[1]);
-        tc::wait_ld();
-        f32x2 x[32];  // keys 2 u and 2 u + 1 of the half
-#pragma unroll
-        for (int u = 0; u < 32; ++u)
-          x[u] = pair2(__uint_as_float(sr[u >> 4][(2 * u) & 31]), __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]));
-        const bool whole = !edge && th >= lo && th + 64 <= hi;
-        float f = 1.f;      // factor of what the row holds
-        bool resc = false;  // O's row holds terms to rescale
-        // The reference m moves, and the row is rescaled, only when a score exceeds it by more than 8, so
-        // weights are at most 2^8. A row that has seen nothing yet exponentiates against 0 (its scores are
-        // -inf, or NaN, which must stay).
-        auto reference = [&](float mx) {
-          const bool move = mx > m_ref + 8.f;
-          resc = move && m_ref != -INFINITY;
-          f = resc ? fast_exp2(m_ref - mx) : 1.f;
-          if (move) m_ref = mx;
-          return m_ref == -INFINITY ? 0.f : -m_ref;
-        };
-        uint32_t pw[32];  // P row as 16-bit pairs
-        float lsum;       // its sum
-        bool near = false;
-        float top = 0.f;
-        if constexpr (CAP) {
-          top = max64(x);
-          const float bottom = -max64neg(x);
-          near = __all_sync(kFull, fmaxf(top * top, bottom * bottom) <= near2);  // the warp's scores: at most half the cap
-          if (cap_in < 0.f) top = bottom;
+    // bring an item's Q into place (the S of the item before have all read theirs), and say so
+    auto start_q = [&](const ScoredItem& i) {
+      int ti, h;
+      const int own = own_row(i, ti, h);
+      const bool shared = shared_rows(i);
+      unsigned char* Qs = smem + (shared ? 0 : w * Sh::QT);
+      if constexpr (Q_AS_F16)  // (both streams need the factors of shared rows)
+        qscale_next = scored_fetch_q_bf16_as_f16<ROWS>(Qs, warp & 3, lane, reinterpret_cast<const __nv_bfloat16*>(p.query),
+                                                       own, !shared || w == 0);
+      else if (!shared || w == 0)
+        scored_fetch_q<T, D, ROWS>(Qs, warp & 3, lane, reinterpret_cast<const T*>(p.query), own);
+    };
+    auto finish_q = [&] {
+      cp_async_wait_all();
+      fence_proxy_async_smem();  // generic-proxy writes, read by the S MMAs
+      mbar_arrive(q_full + w);
+    };
+    bool ok = rows_agree(wait_item(0));
+    if (ok && info(0)->ntile > 0) {
+      start_q(*info(0));
+      finish_q();
+    }
+    for (int k = 0; ok; ++k) {
+      const ScoredItem& m = *info(k);
+      if (m.ntile < 0) {
+        free_item(k);
+        break;
+      }
+      qscale = qscale_next;
+      const bool shared = shared_rows(m);
+      int ti, h;
+      const int orow = own_row(m, ti, h);
+      const bool active = orow >= 0;
+      const int pos = m.ctx - m.q_len + ti;
+      int lo = 0, hi = 0;
+      if (active) scored_span(sc, m.q0 + ti, pos, m.ctx, lo, hi);
+      const int base = scored_base(sc, m.ctx, m.q_len, BS);
+      const int tok0 = base + m.part * P;
+      const RowParts parts = row_parts(lo, hi, base, P);
+      T* out_row = static_cast<T*>(p.out) + (size_t)(active ? orow : 0) * D;
+      if (m.ntile == 0) {  // no key: the zeros of rows that see nothing
+        if (active && parts.last < parts.first && (!shared || w == 0))
+          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out_row + d) = make_uint4(0u, 0u, 0u, 0u);
+        free_item(k);
+        ok = rows_agree(wait_item(k + 1));
+        if (ok && info(k + 1)->ntile > 0) {
+          start_q(*info(k + 1));
+          finish_q();
         }
-        if (!BIAS && __all_sync(kFull, whole) && (CAP ? near : sl2 >= 0.f)) {
+        continue;
+      }
+      const int first = shared ? w : 0, step = shared ? 2 : 1;
+      const float sl2 = p.scale_log2 * qscale;
+      const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
+      const float exp_in = cap_in * 2.8853900817779268f;  // 2 log2(e) / softcap, of a product
+      const float slope = BIAS ? sc.slopes[h] * 1.4426950408889634f : 0.f;
+      // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
+      // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers leave fp32's range.)
+      f32x2 cc[4];
+      float near2 = -1.f;  // the largest x^2 that it is for
+      if constexpr (CAP) {
+        const float z2 = cap_in * cap_in;
+        float c = cap_out * cap_in;
+        const float fit[4] = {0.999999456f, -0.333263179f, 0.131902965f, -0.0444022226f};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          cc[u] = pair2(c * fit[u], c * fit[u]);
+          c *= z2;
+        }
+        if (z2 < 1e6f && z2 > 1e-18f) near2 = 0.25f / z2;
+      }
+      // (FP8 pool: read again where they are used, to keep the 128 registers a thread for the scores: held in
+      // registers they took the causal prompt of 8192 tokens from 571 to 714 us)
+      const int c0_ = m.c0, c1_ = m.c1, ntile_ = m.ntile;
+      auto c0 = [&] { return F8 ? m.c0 : c0_; };
+      auto c1 = [&] { return F8 ? m.c1 : c1_; };
+      auto ntile = [&] { return F8 ? m.ntile : ntile_; };
+      // which blocks of a tile were copied: lane b < NBT holds block b's test (the copying warps' own)
+      auto load_ok = [&](int j) {
+        const int b = c0() / BS + j * NBT + (lane & (NBT - 1));
+        return b < (c1() + BS - 1) / BS &&
+               (unsigned)p.block_tables[(size_t)m.s * p.max_blocks_per_seq + b] < (unsigned)p.num_blocks;
+      };
+      constexpr uint32_t all = (1u << NBT) - 1u;
+      float m_ref = -INFINITY, l = 0.f;
+      int n = 0;
+      bool next = first < ntile() && load_ok(first);
+      for (int j = first; j < ntile(); j += step, ++n, ++cnt) {
+        const uint32_t blocks = __ballot_sync(kFull, next) & all;
+        if (j + step < ntile()) next = load_ok(j + step);
+        const int tb = c0() / BS * BS + j * NT;  // position of the tile's first token
+        const bool edge = blocks != all || tb < c0() || tb + NT > c1();  // V rows outside the item's keys, or not copied
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          const int th = tb + hf * 64;
+          // (tensor-memory accesses are warp-wide: a warp leaves the loop as a whole)
+          ok = __all_sync(kFull, tc_wait(s_full + 2 * w + hf, cnt & 1, abort));
+          if (!ok) break;
+          tc::fence_after_sync();
+          uint32_t sr[2][32];
+          tc::ld32(scol + hf * 64, sr[0]);
+          tc::ld32(scol + hf * 64 + 32, sr[1]);
+          tc::wait_ld();
+          f32x2 x[32];  // keys 2 u and 2 u + 1 of the half
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            x[u] = pair2(__uint_as_float(sr[u >> 4][(2 * u) & 31]), __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]));
+          const bool whole = !edge && th >= lo && th + 64 <= hi;
+          float f = 1.f;      // factor of what the row holds
+          bool resc = false;  // O's row holds terms to rescale
+          // The reference m moves, and the row is rescaled, only when a score exceeds it by more than 8, so
+          // weights are at most 2^8. A row that has seen nothing yet exponentiates against 0 (its scores are
+          // -inf, or NaN, which must stay).
+          auto reference = [&](float mx) {
+            const bool move = mx > m_ref + 8.f;
+            resc = move && m_ref != -INFINITY;
+            f = resc ? fast_exp2(m_ref - mx) : 1.f;
+            if (move) m_ref = mx;
+            return m_ref == -INFINITY ? 0.f : -m_ref;
+          };
+          float lsum;  // of the half's weights
+          bool near = false;
+          float top = 0.f;
           if constexpr (CAP) {
-            const f32x2 t = pair2(top, top), t2 = mul2(t, t);
-            float mx, unused;
-            unpair2(mul2(t, fma2(t2, fma2(t2, fma2(t2, cc[3], cc[2]), cc[1]), cc[0])), mx, unused);
-            const float nm = reference(mx);
-            const f32x2 sub = pair2(nm, nm);
-            lsum = weights64<TP>(pw, [&](int u) {
-              const f32x2 sq = mul2(x[u], x[u]);
-              return fma2(x[u], fma2(sq, fma2(sq, fma2(sq, cc[3], cc[2]), cc[1]), cc[0]), sub);
-            });
-          } else {
-            const float nm = reference(max64(x) * sl2);
-            const f32x2 mul = pair2(sl2, sl2), sub = pair2(nm, nm);
-            lsum = weights64<TP>(pw, [&](int u) { return fma2(x[u], mul, sub); });
+            top = max64(x);
+            const float bottom = -max64neg(x);
+            near = __all_sync(kFull, fmaxf(top * top, bottom * bottom) <= near2);  // the warp's scores: at most half the cap
+            if (cap_in < 0.f) top = bottom;
           }
-        } else {
-          if constexpr (CAP) {
-            if (near) {
+          if (!BIAS && __all_sync(kFull, whole) && (CAP ? near : sl2 >= 0.f)) {
+            if constexpr (CAP) {
+              const f32x2 t = pair2(top, top), t2 = mul2(t, t);
+              float mx, unused;
+              unpair2(mul2(t, fma2(t2, fma2(t2, fma2(t2, cc[3], cc[2]), cc[1]), cc[0])), mx, unused);
+              const float nm = reference(mx);
+              const f32x2 sub = pair2(nm, nm);
+              lsum = weights64<TP>(scol + hf * 64, [&](int u) {
+                const f32x2 sq = mul2(x[u], x[u]);
+                return fma2(x[u], fma2(sq, fma2(sq, fma2(sq, cc[3], cc[2]), cc[1]), cc[0]), sub);
+              });
+            } else {
+              const float nm = reference(max64(x) * sl2);
+              const f32x2 mul = pair2(sl2, sl2), sub = pair2(nm, nm);
+              lsum = weights64<TP>(scol + hf * 64, [&](int u) { return fma2(x[u], mul, sub); });
+            }
+          } else {
+            if constexpr (CAP) {
+              if (near) {
+#pragma unroll
+                for (int u = 0; u < 32; ++u) {
+                  const f32x2 sq = mul2(x[u], x[u]);
+                  x[u] = mul2(x[u], fma2(sq, fma2(sq, fma2(sq, cc[3], cc[2]), cc[1]), cc[0]));
+                }
+              } else {
+#pragma unroll
+                for (int u = 0; u < 32; ++u) {  // cap_out (1 - 2 / (e^(2 z) + 1)): some score is of the cap's size
+                  float v0, v1;
+                  unpair2(mul2(x[u], pair2(exp_in, exp_in)), v0, v1);
+                  unpair2(add2(pair2(fast_exp2(v0), fast_exp2(v1)), pair2(1.f, 1.f)), v0, v1);
+                  x[u] = fma2(pair2(fast_rcp(v0), fast_rcp(v1)), pair2(-2.f * cap_out, -2.f * cap_out), pair2(cap_out, cap_out));
+                }
+              }
+              if constexpr (BIAS) add_bias(x, slope, pos - th);
+            } else if (BIAS && __all_sync(kFull, pos >= th + 63)) {
+              // keys up to the token's own position: -slope (p - j) is linear in j, four chains of steps of 8
+              const f32x2 mul = pair2(sl2, sl2), step8 = pair2(8.f * slope, 8.f * slope);
+              const float d = (float)(th - pos);
+              f32x2 bias[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) bias[k] = pair2(slope * (d + 2 * k), slope * (d + 2 * k + 1));
 #pragma unroll
               for (int u = 0; u < 32; ++u) {
-                const f32x2 sq = mul2(x[u], x[u]);
-                x[u] = mul2(x[u], fma2(sq, fma2(sq, fma2(sq, cc[3], cc[2]), cc[1]), cc[0]));
+                x[u] = fma2(x[u], mul, bias[u & 3]);
+                if (u < 28) bias[u & 3] = add2(bias[u & 3], step8);
               }
             } else {
+              const f32x2 mul = pair2(sl2, sl2);
+#pragma unroll
+              for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], mul);
+              if constexpr (BIAS) add_bias(x, slope, pos - th);
+            }
+            if (!whole) {
+              // bit t of see[i]: the row sees key 32 i + t of the half
+              uint32_t see[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) see[i] = low_bits(hi - th - 32 * i) & ~low_bits(lo - th - 32 * i);
+              if (blocks != all) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int b = 0; b < 32 / BS; ++b)
+                    if (!((blocks >> (hf * (NBT / 2) + i * (32 / BS) + b)) & 1u))
+                      see[i] &= ~((BS == 32 ? 0xffffffffu : (1u << (BS & 31)) - 1u) << (b * BS));
+              }
 #pragma unroll
               for (int u = 0; u < 32; ++u) {
                 float v0, v1;
                 unpair2(x[u], v0, v1);
-                x[u] = pair2(cap_out * score_tanh(v0 * cap_in), cap_out * score_tanh(v1 * cap_in));
+                const uint32_t bits = see[u >> 4];
+                x[u] = pair2(bits & (1u << ((2 * u) & 31)) ? v0 : -INFINITY,
+                             bits & (1u << ((2 * u + 1) & 31)) ? v1 : -INFINITY);
               }
             }
-            if constexpr (BIAS) add_bias(x, slope, pos - th);
-          } else if (BIAS && __all_sync(kFull, pos >= th + 63)) {
-            // keys up to the token's own position: -slope (p - j) is linear in j, four chains of steps of 8
-            const f32x2 mul = pair2(sl2, sl2), step8 = pair2(8.f * slope, 8.f * slope);
-            const float d = (float)(th - pos);
-            f32x2 bias[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) bias[k] = pair2(slope * (d + 2 * k), slope * (d + 2 * k + 1));
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              x[u] = fma2(x[u], mul, bias[u & 3]);
-              if (u < 28) bias[u & 3] = add2(bias[u & 3], step8);
-            }
-          } else {
-            const f32x2 mul = pair2(sl2, sl2);
-#pragma unroll
-            for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], mul);
-            if constexpr (BIAS) add_bias(x, slope, pos - th);
+            const float nm = reference(max64(x));
+            const f32x2 sub = pair2(nm, nm);
+            lsum = weights64<TP>(scol + hf * 64, [&](int u) { return add2(x[u], sub); });
           }
-          if (!whole) {
-            const uint32_t hb = blocks >> (hf * (NBT / 2));
-            const int a = lo - th;
-            const unsigned len = (unsigned)(hi - lo);
+          l = l * f + lsum;
+          if (__any_sync(kFull, resc)) {  // the whole warp moves its rows' O (factor 1 for rows that keep theirs)
+            // the half two before is done (its P's columns hold this S); the one before may still be multiplied
+            // (a row that moves has seen keys, so there is one)
+            ok = __all_sync(kFull, hf ? tc_wait(pv_done + 2 * w, cnt & 1, abort)
+                                      : n == 0 || tc_wait(pv_done + 2 * w + 1, (cnt - 1) & 1, abort));
+            if (!ok) break;
+            tc::fence_after_sync();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              float v0, v1;
-              unpair2(x[u], v0, v1);
-              const bool there = (hb >> (2 * u / BS)) & 1u;
-              x[u] = pair2(there && (unsigned)(2 * u - a) < len ? v0 : -INFINITY,
-                           there && (unsigned)(2 * u + 1 - a) < len ? v1 : -INFINITY);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::ld32(ocol + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              tc::st32(ocol + c * 32, o);
             }
           }
-          const float nm = reference(max64(x));
-          const f32x2 sub = pair2(nm, nm);
-          lsum = weights64<TP>(pw, [&](int u) { return add2(x[u], sub); });
-        }
-        if (__any_sync(kFull, resc)) {  // the whole warp moves its rows' O (factor 1 for rows that keep theirs)
-          // the half two before is done (its P's columns hold this S); the one before may still be multiplied
-          // (a row that moves has seen keys, so there is one)
-          ok = __all_sync(kFull, hf ? tc_wait(pv_done + 2 * w, n & 1, abort)
-                                    : n == 0 || tc_wait(pv_done + 2 * w + 1, (n - 1) & 1, abort));
-          if (!ok) break;
-          tc::fence_after_sync();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc::ld32(ocol + c * 32, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-            tc::st32(ocol + c * 32, o);
+          tc::wait_st();
+          // V rows that were not copied, or lie outside the CTA's keys, may hold anything (NaN): zero them once
+          // V has landed, since P = 0 times NaN is NaN in the MMA
+          if (edge && hf == 0) {
+            const int iv = 2 * (tiles + j) + 1;
+            ok = __all_sync(kFull, tc_wait(full + iv % NS, (iv / NS) & 1, abort));
+            if (!ok) break;
+            unsigned char* vs = slot(iv);
+            for (int i = threadIdx.x & 127; i < NT * 8 * Sh::DH; i += 128) {
+              const int t = i / (8 * Sh::DH), c = i % (8 * Sh::DH);
+              if (!((blocks >> (t / BS)) & 1u) || tb + t >= c1() || tb + t < c0())
+                *reinterpret_cast<uint4*>(vs + (t / 8) * Sh::ATOM + (c / 8) * 1024 + tc::sw128(t % 8, c % 8)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // the zeros precede the PV's reads
           }
+          tc::fence_before_sync();
+          mbar_arrive(p_full + 2 * w + hf);
         }
-        l = l * f + lsum;
-        tc::st32(scol + hf * 64, pw);  // P over S
-        tc::wait_st();
-        // V rows that were not copied, or lie outside the CTA's keys, may hold anything (NaN): zero them once
-        // V has landed, since P = 0 times NaN is NaN in the MMA
-        if (edge && hf == 0) {
-          const int iv = 2 * j + 1;
-          ok = __all_sync(kFull, tc_wait(full + iv % NS, (iv / NS) & 1, abort));
-          if (!ok) break;
-          unsigned char* vs = slot(iv);
-          for (int i = threadIdx.x & 127; i < NT * 8 * Sh::DH; i += 128) {
-            const int t = i / (8 * Sh::DH), c = i % (8 * Sh::DH);
-            if (!((blocks >> (t / BS)) & 1u) || tb + t >= c1 || tb + t < c0)
-              *reinterpret_cast<uint4*>(vs + (t / 8) * Sh::ATOM + (c / 8) * 1024 + tc::sw128(t % 8, c % 8)) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();  // the zeros precede the PV's reads
+        if (!ok) break;
+      }
+      // ---- the next item's Q: this stream's S have all been read (of shared rows: both streams', below)
+      bool going = false;
+      auto next_q = [&] {
+        going = wait_item(k + 1);
+        if (going && info(k + 1)->ntile > 0) {
+          start_q(*info(k + 1));
+          if (Q_AS_F16) finish_q();
+        }
+      };
+      if (ok && !shared) next_q();
+      // ---- epilogue: O / l
+      if (ok && n > 0)
+        ok = __all_sync(kFull, tc_wait(pv_done + 2 * w, (cnt - 1) & 1, abort) &&
+                                   tc_wait(pv_done + 2 * w + 1, (cnt - 1) & 1, abort));
+      tc::fence_after_sync();
+      float f0 = 1.f, f1 = 0.f;  // factors of this stream's O and of the other's (shared rows)
+      bool other = false;        // the other stream has an O
+      if (shared) {  // stream 1 hands its (m, l) over; its O stays where it is until the item's end
+        if (w == 1) {
+          ml[row] = ok && n > 0 ? m_ref : -INFINITY;
+          ml[ROWS + row] = ok && n > 0 ? l : 0.f;
         }
         tc::fence_before_sync();
-        mbar_arrive(p_full + 2 * w + hf);
+        ok = rows_agree(ok);
+        tc::fence_after_sync();
+        if (w == 0) {
+          other = m.ntile > 1;
+          const float m1 = ml[row], l1 = ml[ROWS + row];
+          const float M = fmaxf(m_ref, m1), Ms = M == -INFINITY ? 0.f : M;
+          f0 = m_ref == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_ref - Ms);
+          f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : fast_exp2(m1 - Ms);
+          l = l * f0 + l1 * f1;
+          m_ref = M;
+        }
       }
-      if (!ok) break;
-    }
-    // ---- epilogue: O / l
-    if (ok && n > 0)
-      ok = __all_sync(kFull, tc_wait(pv_done + 2 * w, (n - 1) & 1, abort) &&
-                                 tc_wait(pv_done + 2 * w + 1, (n - 1) & 1, abort));
-    tc::fence_after_sync();
-    float f0 = 1.f, f1 = 0.f;  // factors of this stream's O and of the other's (shared rows)
-    float* stage = reinterpret_cast<float*>(smem + Sh::OFF_RING);  // [D][128]: the other stream's O
-    float* ml = reinterpret_cast<float*>(smem + Sh::OFF_ML);
-    if (shared_rows) {
-      // stream 1 hands its (m, l, O) over; every slot has been read, for both streams' PV are done
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      if (w == 1) {
-        ml[row] = ok && n > 0 ? m_ref : -INFINITY;
-        ml[ROWS + row] = ok && n > 0 ? l : 0.f;
-        if (ok && n > 0) {
+      if (ok && shared) next_q();
+      if (!Q_AS_F16 && going && info(k + 1)->ntile > 0) finish_q();
+      if (!shared || w == 0) {
+        const bool mine = active && parts.in(m.part), direct = parts.direct();
+        // 1 / l (FP8 pool: times the value of one V code)
+        const float inv = ok && l != 0.f ? (F8 ? p.v_scale : 1.f) / l : 0.f;
+        bool fine = true;
+        int quad_row[4];  // the rows of this lane's quad that go to the output; -1: not
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc::ld32(ocol + c * 32, o);
+        for (int i = 0; i < 4; ++i) quad_row[i] = __shfl_sync(kFull, mine && direct ? orow : -1, (lane & ~3) + i);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc::ld32(ocol + c * 32, o);
+          tc::wait_ld();
+          float v[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(o[u]);
+          if (other) {
+            tc::ld32(ocol + 128 + c * 32, o);
             tc::wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) stage[(c * 32 + u) * ROWS + row] = __uint_as_float(o[u]);
+            for (int u = 0; u < 32; ++u) v[u] = f0 * v[u] + f1 * __uint_as_float(o[u]);
           }
-        } else {
-          for (int d = 0; d < D; ++d) stage[d * ROWS + row] = 0.f;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            v[u] = ok ? v[u] * inv : 0.f;
+            fine = fine && fabsf(v[u]) < INFINITY;
+          }
+          uint32_t o16[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o16[u] = Elem<T>::pack2(v[2 * u], v[2 * u + 1]);
+          quad_transpose(o16, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (quad_row[i] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)quad_row[i] * D + c * 32 + (lane & 3) * 8) =
+                  make_uint4(o16[4 * i], o16[4 * i + 1], o16[4 * i + 2], o16[4 * i + 3]);
+          if (mine && !direct) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + ((size_t)orow * p.max_partitions + m.part) * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
+        }
+        if (mine && !direct) {
+          p.part_m[(size_t)orow * p.max_partitions + m.part] = ok ? m_ref : -INFINITY;
+          p.part_l[(size_t)orow * p.max_partitions + m.part] = ok ? l : 0.f;
+        }
+        // rows that came out non-finite: again, key by key, on the whole warp
+        for (uint32_t redo = __ballot_sync(kFull, mine && !fine); redo; redo &= redo - 1) {
+          const int src = __ffs(redo) - 1;
+          const int rlo = __shfl_sync(kFull, lo, src), rhi = __shfl_sync(kFull, hi, src);
+          const int rpos = __shfl_sync(kFull, pos, src), rh = __shfl_sync(kFull, h, src);
+          const int at = __shfl_sync(kFull, orow, src);
+          const bool rdirect = __shfl_sync(kFull, (int)direct, src);
+          float rm, rl, o[D / 32];
+          scored_row<T, C, D>(p, sc, at, m.s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o);
+          store_row<T, D>(p, at, m.part, rdirect, lane, rm, rl, o);
         }
       }
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      if (w == 0) {
-        const float m1 = ml[row], l1 = ml[ROWS + row];
-        const float M = fmaxf(m_ref, m1), Ms = M == -INFINITY ? 0.f : M;
-        f0 = m_ref == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m_ref - Ms);
-        f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : fast_exp2(m1 - Ms);
-        l = l * f0 + l1 * f1;
-        m_ref = M;
-      }
-    }
-    ok = ok && !*abort;
-    if (!shared_rows || w == 0) {
-      const bool mine = active && parts.in(part), direct = parts.direct();
-      const size_t orow = (size_t)(q0 + ti) * p.num_heads + h;
-      // 1 / l (FP8 pool: times the value of one V code)
-      const float inv = ok && l != 0.f ? (F8 ? p.v_scale : 1.f) / l : 0.f;
-      bool fine = true;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tc::ld32(ocol + c * 32, o);
-        tc::wait_ld();
-        float v[32];
-#pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          v[u] = __uint_as_float(o[u]);
-          if (shared_rows) v[u] = f0 * v[u] + f1 * stage[(c * 32 + u) * ROWS + row];
-          v[u] = ok ? v[u] * inv : 0.f;
-          fine = fine && fabsf(v[u]) < INFINITY;
-        }
-        if (!mine) continue;
-        if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(out_row + c * 32);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            dst[u] = make_uint4(Elem<T>::pack2(v[8 * u], v[8 * u + 1]), Elem<T>::pack2(v[8 * u + 2], v[8 * u + 3]),
-                                Elem<T>::pack2(v[8 * u + 4], v[8 * u + 5]), Elem<T>::pack2(v[8 * u + 6], v[8 * u + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.max_partitions + part) * D + c * 32);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) dst[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        }
-      }
-      if (mine && !direct) {
-        p.part_m[orow * p.max_partitions + part] = ok ? m_ref : -INFINITY;
-        p.part_l[orow * p.max_partitions + part] = ok ? l : 0.f;
-      }
-      // rows that came out non-finite: again, key by key, on the whole warp
-      for (uint32_t redo = __ballot_sync(kFull, mine && !fine); redo; redo &= redo - 1) {
-        const int src = __ffs(redo) - 1;
-        const int rlo = __shfl_sync(kFull, lo, src), rhi = __shfl_sync(kFull, hi, src);
-        const int rpos = __shfl_sync(kFull, pos, src), rh = __shfl_sync(kFull, h, src);
-        const int rti = __shfl_sync(kFull, ti, src);
-        const bool rdirect = __shfl_sync(kFull, (int)direct, src);
-        const size_t at = (size_t)(q0 + rti) * p.num_heads + rh;
-        float m, ll, o[D / 32];
-        scored_row<T, C, D>(p, sc, at, s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, m, ll, o);
-        store_row<T, D>(p, at, part, rdirect, lane, m, ll, o);
-      }
+      // both streams go on together (stream 1's O has been read), or leave together
+      tc::fence_before_sync();
+      ok = rows_agree(ok && going);
+      tc::fence_after_sync();
+      tiles += m.ntile;
+      free_item(k);
     }
   }
 
