@@ -463,98 +463,120 @@ def paged_attention_scored_workspace_size(num_query_tokens: int, num_heads: int,
                                                             partition_size))
 
 
-def _launch(fn, device: torch.device, stream, *args) -> None:
-    """Call fn(*args, stream handle) with the tensors' device current (the library launches on the current one)."""
-    index = device.index
-    if index is None or index == torch.cuda.current_device():
-        handle = _stream_of(device, stream)
+def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int) -> None:
+    """t must be a contiguous tensor of this type on CUDA device dev."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        if not t.is_cuda:
+            raise PagedKVError(-1, f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise PagedKVError(-1, f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+        if t.dtype is not dtype:
+            raise PagedKVError(-1, f"{name} must be {dtype}, got {t.dtype}")
+        raise PagedKVError(-1, f"{name} must be contiguous")
+
+
+def _run_on(dev: int, stream, fn, args) -> None:
+    """fn(*args, stream handle) with device dev current (the library launches on the current device)."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, _stream_of(device, stream))
-    if status != 0:
-        _check(load(), status)
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status:
+        _check(_lib, status)
 
 
-def _stream_of(device: torch.device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _same_device(first: torch.Tensor, **tensors) -> None:
-    for n, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise PagedKVError(-1, f"{n} is on {t.device}, query and tables on {first.device}")
-
-
+# These checks run on every call, and a small call is bound by them: each tensor's type, device and layout are
+# tested in one expression, and the reasons are looked for only when one fails.
 def _scored(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale, softcap,
             alibi_slopes, window, key_begin, key_end, max_query_len, max_context_len, partition_size, workspace,
             stream, fp8, k_scale, v_scale):
-    lib = load()
-    dt = _cuda16("query", query)
-    if _cuda16("out", out) != dt:
-        raise PagedKVError(-1, "out dtype differs from query")
-    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if fp8:
+    lib = _lib or load()
+    dtype = query.dtype
+    dt = _DTYPE.get(dtype)
+    dev = query.get_device()
+    if dt is None or dev < 0 or not query.is_contiguous():
+        _cuda16("query", query)
+    _expect("out", out, dtype, dev)
+    if fp8:
+        for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
             _cuda_fp8(n, t)
-        elif _cuda16(n, t) != dt:
-            raise PagedKVError(-1, f"{n} dtype differs from query")
-    _cuda_i32("block_tables", block_tables)
-    _cuda_i32("context_lens", context_lens)
-    if key_cache.dim() != 4 or query.dim() != 3:
-        raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim] and query [rows][heads][head dim]")
-    NB, Hkv, B, D = key_cache.shape
-    T, H, D2 = query.shape
-    if D2 != D or out.shape != query.shape or value_cache.shape != key_cache.shape:
+            _expect(n, t, t.dtype, dev)
+    else:
+        _expect("key_cache", key_cache, dtype, dev)
+        _expect("value_cache", value_cache, dtype, dev)
+    _expect("block_tables", block_tables, torch.int32, dev)
+    _expect("context_lens", context_lens, torch.int32, dev)
+    shape, pool, tables = query.shape, key_cache.shape, block_tables.shape
+    if len(pool) != 4 or len(shape) != 3 or len(tables) != 2:
+        raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim], query [rows][heads][head "
+                               "dim] and block_tables [S][max_blocks]")
+    NB, Hkv, B, D = pool
+    T, H, D2 = shape
+    S, maxb = tables
+    if D2 != D or out.shape != shape or value_cache.shape != pool:
         raise PagedKVError(-1, "shape mismatch between query, out and caches")
-    S = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1:
+    if context_lens.shape != (S,):
         raise PagedKVError(-1, "block_tables must be [S][max_blocks] and context_lens [S]")
-    decode = query_start_loc is None
-    if decode:
+    if query_start_loc is None:
         if T != S:
             raise PagedKVError(-1, f"query has {T} rows for {S} sequences")
         max_query_len = 1
     else:
-        _cuda_i32("query_start_loc", query_start_loc)
+        _expect("query_start_loc", query_start_loc, torch.int32, dev)
         if query_start_loc.shape != (S + 1,):
             raise PagedKVError(-1, "query_start_loc must be [S + 1]")
         if max_query_len is None:
             max_query_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
-    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_cuda
-                                     or not alibi_slopes.is_contiguous() or alibi_slopes.shape != (H,)):
-        raise PagedKVError(-1, "alibi_slopes must be a contiguous CUDA float32 tensor [num_heads]")
-    for n, t in (("key_begin", key_begin), ("key_end", key_end)):
-        if t is not None:
-            _cuda_i32(n, t)
-            if t.shape != (T,):
-                raise PagedKVError(-1, f"{n} must have one entry per query row")
-    _same_device(query, out=out, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
-                 context_lens=context_lens, query_start_loc=query_start_loc, alibi_slopes=alibi_slopes,
-                 key_begin=key_begin, key_end=key_end, workspace=workspace)
-    maxb = block_tables.shape[1]
+    slopes = begin = end = ws = None
+    if alibi_slopes is not None:
+        _expect("alibi_slopes", alibi_slopes, torch.float32, dev)
+        if alibi_slopes.shape != (H,):
+            raise PagedKVError(-1, "alibi_slopes must have one entry per head")
+        slopes = alibi_slopes.data_ptr()
+    if key_begin is not None:
+        _expect("key_begin", key_begin, torch.int32, dev)
+        if key_begin.shape != (T,):
+            raise PagedKVError(-1, "key_begin must have one entry per query row")
+        begin = key_begin.data_ptr()
+    if key_end is not None:
+        _expect("key_end", key_end, torch.int32, dev)
+        if key_end.shape != (T,):
+            raise PagedKVError(-1, "key_end must have one entry per query row")
+        end = key_end.data_ptr()
     if max_context_len is None:
         max_context_len = maxb * B
-    if workspace is None:
-        need = int(lib.paged_attention_scored_workspace_size(T, H, Hkv, D, B, int(max_query_len), int(max_context_len),
-                                                             int(window), int(partition_size)))
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    head = (_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), maxb, _ptr(context_lens))
-    rules = (float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(key_begin))
-    shape = (B, H, Hkv, D, NB, dt) + ((float(k_scale), float(v_scale)) if fp8 else ())
-    work = (int(partition_size), _ptr(workspace), wbytes)
-    if decode:
-        fn = lib.paged_attention_decode_scored_fp8 if fp8 else lib.paged_attention_decode_scored
-        _launch(fn, query.device, stream, *head, S, int(max_context_len), *rules, *shape, *work)
+    wbytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise PagedKVError(-1, "workspace must be a contiguous tensor on the query's device")
+        wbytes = workspace.numel() * workspace.element_size()
     else:
-        fn = lib.paged_attention_multi_query_scored_fp8 if fp8 else lib.paged_attention_multi_query_scored
-        _launch(fn, query.device, stream, *head, _ptr(query_start_loc), S, T, int(max_query_len),
-                int(max_context_len), *rules, _ptr(key_end), *shape, *work)
+        wbytes = lib.paged_attention_scored_workspace_size(T, H, Hkv, D, B, max_query_len, max_context_len, window,
+                                                           partition_size)
+        if wbytes:
+            workspace = torch.empty(wbytes, dtype=torch.uint8, device=query.device)
+    if workspace is not None:
+        ws = workspace.data_ptr()
+    scales = (k_scale, v_scale) if fp8 else ()
+    if query_start_loc is None:
+        _run_on(dev, stream, lib.paged_attention_decode_scored_fp8 if fp8 else lib.paged_attention_decode_scored,
+                (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                 block_tables.data_ptr(), maxb, context_lens.data_ptr(), S, max_context_len, scale, softcap, slopes,
+                 window, begin, B, H, Hkv, D, NB, dt, *scales, partition_size, ws, wbytes))
+    else:
+        _run_on(dev, stream,
+                lib.paged_attention_multi_query_scored_fp8 if fp8 else lib.paged_attention_multi_query_scored,
+                (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                 block_tables.data_ptr(), maxb, context_lens.data_ptr(), query_start_loc.data_ptr(), S, T,
+                 max_query_len, max_context_len, scale, softcap, slopes, window, begin, end, B, H, Hkv, D, NB, dt,
+                 *scales, partition_size, ws, wbytes))
     return out
 
 
@@ -619,23 +641,28 @@ def paged_attention_multi_query_scored_fp8(out: torch.Tensor, query: torch.Tenso
                    workspace, stream, True, k_scale, v_scale)
 
 
-def _pool_arrays(block_tables, context_lens, lens_name, lens, free_blocks, num_free, **outs) -> int:
-    """Check the arrays that the reserve and release calls share; returns the number of sequences."""
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), (lens_name, lens),
-                 ("free_blocks", free_blocks), ("num_free", num_free), *outs.items()):
-        _cuda_i32(n, t)
-    S = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1 or lens.shape != (S,):
-        raise PagedKVError(-1, f"block_tables must be [S][max_blocks], context_lens and {lens_name} [S]")
-    if free_blocks.dim() != 1 or num_free.numel() != 1 or outs["num_free_out"].numel() != 1:
+def _pool_arrays(block_tables, context_lens, lens_name, lens, free_blocks, num_free, context_lens_out, num_free_out):
+    """Check the arrays that the reserve and release calls share; returns (sequences, table width, device)."""
+    dev = block_tables.get_device()
+    i32 = torch.int32
+    if dev < 0:
+        _cuda_i32("block_tables", block_tables)
+    _expect("block_tables", block_tables, i32, dev)
+    _expect("context_lens", context_lens, i32, dev)
+    _expect(lens_name, lens, i32, dev)
+    _expect("free_blocks", free_blocks, i32, dev)
+    _expect("num_free", num_free, i32, dev)
+    _expect("context_lens_out", context_lens_out, i32, dev)
+    _expect("num_free_out", num_free_out, i32, dev)
+    tables = block_tables.shape
+    if len(tables) != 2:
+        raise PagedKVError(-1, "block_tables must be [S][max_blocks]")
+    S, maxb = tables
+    if context_lens.shape != (S,) or lens.shape != (S,) or context_lens_out.shape != (S,):
+        raise PagedKVError(-1, f"context_lens, {lens_name} and context_lens_out must be [S]")
+    if free_blocks.dim() != 1 or num_free.numel() != 1 or num_free_out.numel() != 1:
         raise PagedKVError(-1, "free_blocks must be a vector, num_free and num_free_out one element")
-    for n, t in outs.items():
-        want = S + 1 if n == "query_start_loc" else 1 if n == "num_free_out" else S
-        if t.numel() != want:
-            raise PagedKVError(-1, f"{n} must have {want} elements")
-    _same_device(block_tables, context_lens=context_lens, free_blocks=free_blocks, num_free=num_free,
-                 **{lens_name: lens}, **outs)
-    return S
+    return S, maxb, dev
 
 
 def paged_kv_reserve_slots(block_tables: torch.Tensor, context_lens: torch.Tensor, new_lens: torch.Tensor,
@@ -647,17 +674,19 @@ def paged_kv_reserve_slots(block_tables: torch.Tensor, context_lens: torch.Tenso
     free_blocks[:num_free]: updates block_tables in place and writes slot_mapping [max_tokens] int64 (-1: padding,
     or a sequence that got nothing), query_start_loc [S + 1], context_lens_out [S], num_free_out [1] and granted [S].
     The outputs must not overlap the inputs."""
-    lib = load()
-    S = _pool_arrays(block_tables, context_lens, "new_lens", new_lens, free_blocks, num_free,
-                     query_start_loc=query_start_loc, context_lens_out=context_lens_out, num_free_out=num_free_out,
-                     granted=granted)
-    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_cuda or not slot_mapping.is_contiguous():
-        raise PagedKVError(-1, "slot_mapping must be a contiguous CUDA int64 tensor")
-    _same_device(block_tables, slot_mapping=slot_mapping)
-    _launch(lib.paged_kv_reserve_slots, block_tables.device, stream, _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), _ptr(new_lens), _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
-            _ptr(slot_mapping), slot_mapping.numel(), _ptr(query_start_loc), _ptr(context_lens_out),
-            _ptr(num_free_out), _ptr(granted), S, int(block_size), int(num_blocks))
+    lib = _lib or load()
+    S, maxb, dev = _pool_arrays(block_tables, context_lens, "new_lens", new_lens, free_blocks, num_free,
+                                context_lens_out, num_free_out)
+    _expect("query_start_loc", query_start_loc, torch.int32, dev)
+    _expect("granted", granted, torch.int32, dev)
+    _expect("slot_mapping", slot_mapping, torch.int64, dev)
+    if query_start_loc.shape != (S + 1,) or granted.shape != (S,):
+        raise PagedKVError(-1, "query_start_loc must be [S + 1] and granted [S]")
+    _run_on(dev, stream, lib.paged_kv_reserve_slots,
+            (block_tables.data_ptr(), maxb, context_lens.data_ptr(), new_lens.data_ptr(), free_blocks.data_ptr(),
+             free_blocks.numel(), num_free.data_ptr(), slot_mapping.data_ptr(), slot_mapping.numel(),
+             query_start_loc.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(), granted.data_ptr(), S,
+             block_size, num_blocks))
 
 
 def paged_kv_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, finished: torch.Tensor,
@@ -665,12 +694,13 @@ def paged_kv_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tens
                             num_free_out: torch.Tensor, block_size: int, num_blocks: int, stream=None) -> None:
     """Push the blocks of the sequences with finished[s] != 0 on the free stack free_blocks (in place), and write
     context_lens_out [S] (0 for them) and num_free_out [1]. The outputs must not overlap the inputs."""
-    lib = load()
-    S = _pool_arrays(block_tables, context_lens, "finished", finished, free_blocks, num_free,
-                     context_lens_out=context_lens_out, num_free_out=num_free_out)
-    _launch(lib.paged_kv_release_blocks, block_tables.device, stream, _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), _ptr(finished), _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
-            _ptr(context_lens_out), _ptr(num_free_out), S, int(block_size), int(num_blocks))
+    lib = _lib or load()
+    S, maxb, dev = _pool_arrays(block_tables, context_lens, "finished", finished, free_blocks, num_free,
+                                context_lens_out, num_free_out)
+    _run_on(dev, stream, lib.paged_kv_release_blocks,
+            (block_tables.data_ptr(), maxb, context_lens.data_ptr(), finished.data_ptr(), free_blocks.data_ptr(),
+             free_blocks.numel(), num_free.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(), S,
+             block_size, num_blocks))
 
 
 def device_errors(clear: bool = True) -> int:

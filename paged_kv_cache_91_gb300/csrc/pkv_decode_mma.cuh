@@ -61,18 +61,25 @@ __device__ __forceinline__ void copy_tile16(unsigned char* dst, const CUtensorMa
   }
 }
 
-// What a tile's fold() does with a raw product: rule(c, x, t, in) is the score, in the base-2 domain, of the
-// lane's column c (0 or 1) with token t of the tile, -inf where the column does not see it (`in`: t is among
-// the tile's valid tokens). HOLES: a column may see no token of a tile, or of all tiles so far.
+// What a tile's fold() does with its raw products: rule(x, ta, va, tb, vb) turns the lane's four (column 0 and
+// column 1 with token ta of the tile, then with token tb) into scores in the base-2 domain, -inf where the
+// column does not see the token (va, vb: it is among the tile's valid tokens). HOLES: a column may see no token
+// of a tile, or of all tiles so far.
 // This rule scales; with CAUSAL a column also sees only tokens whose position tok_base + t is below its limit.
 template <bool CAUSAL>
 struct ScaleRule {
   static constexpr bool HOLES = CAUSAL;
   float sla, slb;
   int tok_base, lim0, lim1;
-  __device__ __forceinline__ float operator()(int c, float x, int t, bool in) const {
+  __device__ __forceinline__ float one(int c, float x, int t, bool in) const {
     if constexpr (CAUSAL) in = in && tok_base + t < (c ? lim1 : lim0);
     return in ? x * (c ? slb : sla) : -INFINITY;
+  }
+  __device__ __forceinline__ void operator()(float (&x)[4], int ta, bool va, int tb, bool vb) const {
+    x[0] = one(0, x[0], ta, va);
+    x[1] = one(1, x[1], ta, va);
+    x[2] = one(0, x[2], tb, vb);
+    x[3] = one(1, x[3], tb, vb);
   }
 };
 
@@ -181,10 +188,8 @@ struct MmaTile {
         const int ta = c * 16 + r0, tb = ta + 8;
         const bool va = (BS >= 16 || r0 < BS) && ta < nvalid && ta >= first;
         const bool vb = BS >= 16 && tb < nvalid && tb >= first;
-        const float x00 = rule(0, sacc[0], ta, va);
-        const float x01 = rule(1, sacc[1], ta, va);
-        const float x10 = rule(0, sacc[2], tb, vb);
-        const float x11 = rule(1, sacc[3], tb, vb);
+        rule(sacc, ta, va, tb, vb);
+        const float x00 = sacc[0], x01 = sacc[1], x10 = sacc[2], x11 = sacc[3];
         // Lazy rescaling: a column's reference m moves (and its state is rescaled) only when one of its
         // scores exceeds m by more than 8, so p = 2^(x - m) <= 2^8. Each lane tests its own scores and the
         // warp votes; the max is reduced across the lanes only when some score does exceed.

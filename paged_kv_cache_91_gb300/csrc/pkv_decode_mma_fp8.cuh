@@ -199,10 +199,8 @@ struct MmaTileE4M3 {
         for (int e = 0; e < 4; ++e) sacc[e] += sacc2[e];
         const bool va = ta < nvalid && ta >= first;
         const bool vb = BS >= 16 && ta + 8 < nvalid && ta + 8 >= first;
-        const float x00 = rule(0, sacc[0], ta, va);
-        const float x01 = rule(1, sacc[1], ta, va);
-        const float x10 = rule(0, sacc[2], ta + 8, vb);
-        const float x11 = rule(1, sacc[3], ta + 8, vb);
+        rule(sacc, ta, va, ta + 8, vb);
+        const float x00 = sacc[0], x01 = sacc[1], x10 = sacc[2], x11 = sacc[3];
         // Lazy rescaling: a column's reference m moves (and its state is rescaled)
         // only when a score exceeds it by more than 8, so p = 2^(x - m) <= 2^8. Each
         // lane tests its own scores and the warp votes; the max is reduced across

@@ -28,6 +28,12 @@ struct ScoreParams {
   const int32_t* order = nullptr;       // if set, the sequence of grid index z (longest context first)
 };
 
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // tanh(z): below 1 an odd polynomial, a minimax fit of tanh(z) / z in z^2 on [0, 1] (relative error 5e-8);
 // above, 1 - 2 / (e^(2 z) + 1), whose cancellation costs nothing there (|tanh| > 0.76). tanh.approx has a
 // relative error of 2^-11, which at a cap of 50 would move a score by up to 0.02.

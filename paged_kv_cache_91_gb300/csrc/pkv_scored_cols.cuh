@@ -18,16 +18,53 @@ struct ScoredRule {
   static constexpr bool HOLES = true;
   float mul0, mul1;      // of the raw product: scale * log2(e), or scale / softcap
   float cap_out;         // softcap * log2(e), 0: no cap
+  bool biased;
   float slope0, slope1;  // times log2(e)
   int lo0, n0, lo1, n1;  // the columns' visible keys [lo, lo + n)
   int pos0, pos1;        // the columns' positions
   int tok_base;          // position of the tile's token 0
-  __device__ __forceinline__ float operator()(int c, float x, int t, bool in) const {
-    const int j = tok_base + t;
-    float y = x * (c ? mul1 : mul0);
-    if (cap_out != 0.f) y = cap_out * score_tanh(y);
-    y -= (c ? slope1 : slope0) * fabsf((float)((c ? pos1 : pos0) - j));
-    return in && (unsigned)(j - (c ? lo1 : lo0)) < (unsigned)(c ? n1 : n0) ? y : -INFINITY;
+  bool whole;            // every column of the warp sees every token of the tile
+  __device__ __forceinline__ void operator()(float (&x)[4], int ta, bool va, int tb, bool vb) const {
+    const int ja = tok_base + ta, jb = tok_base + tb;
+    bool see[4] = {true, true, true, true};
+    if (!whole) {
+      see[0] = va && (unsigned)(ja - lo0) < (unsigned)n0;
+      see[1] = va && (unsigned)(ja - lo1) < (unsigned)n1;
+      see[2] = vb && (unsigned)(jb - lo0) < (unsigned)n0;
+      see[3] = vb && (unsigned)(jb - lo1) < (unsigned)n1;
+    }
+    x[0] *= mul0;
+    x[1] *= mul1;
+    x[2] *= mul0;
+    x[3] *= mul1;
+    if (cap_out != 0.f) {
+      float z = 0.f;  // (of the keys that are seen: the others may hold anything)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z = fmaxf(z, see[e] ? fabsf(x[e]) : 0.f);
+      if (__all_sync(kFull, z <= 0.5f)) {
+        // tanh(z) / z in z^2 on [0, 1/4]: a minimax fit, relative error 6e-7
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[e] * x[e];
+          const float q = fmaf(u, fmaf(u, fmaf(u, -0.0444022226f, 0.131902965f), -0.333263179f), 0.999999456f);
+          x[e] = cap_out * (x[e] * q);
+        }
+      } else {  // some score is of the cap's size: the cancellation of 1 - 2 / (e^(2 z) + 1) is small beside it
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = cap_out - 2.f * cap_out * fast_rcp(fast_exp2(x[e] * 2.8853900817779268f) + 1.f);
+      }
+    }
+    if (biased) {
+      x[0] = fmaf(-slope0, fabsf((float)(pos0 - ja)), x[0]);
+      x[1] = fmaf(-slope1, fabsf((float)(pos1 - ja)), x[1]);
+      x[2] = fmaf(-slope0, fabsf((float)(pos0 - jb)), x[2]);
+      x[3] = fmaf(-slope1, fabsf((float)(pos1 - jb)), x[3]);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = see[e] ? x[e] : -INFINITY;
+    }
   }
 };
 
@@ -146,6 +183,7 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
     const float mul = sc.cap_out != 0.f ? sc.cap_in : p.scale_log2;
     const float slope = sc.slopes ? sc.slopes[hn] * 1.4426950408889634f : 0.f;
     rule.cap_out = sc.cap_out;
+    rule.biased = sc.slopes != nullptr;
     rule.mul0 = mul * fa;
     rule.mul1 = mul * fb;
     rule.slope0 = __shfl_sync(kFull, slope, 4 * j0);
@@ -176,6 +214,9 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
       unsigned char* Ks = ring + k * Sh::STAGE;
       rule.tok_base = (blk0 + warp + NW * i) * BS;
       const int first = max(0, c0 - rule.tok_base), nvalid = min(BS, c1 - rule.tok_base);
+      // (a tile of 8 tokens fills half of the MMA's rows: its other rows are masked)
+      rule.whole = BS >= 16 && first == 0 && nvalid == BS &&
+                   __all_sync(kFull, lo <= rule.tok_base && rule.tok_base + BS <= hi);
       Tile::fold(Ks, Ks + Sh::TILE, first, nvalid, qb, lane, m0, m1, l0, l1, acc, rule);
       if (first > 0 || nvalid < BS) zeroed |= 1u << k;
     }

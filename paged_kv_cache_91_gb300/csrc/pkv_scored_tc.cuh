@@ -68,11 +68,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // The largest of 64 values held as pairs, and of their negatives (four chains of three-way maxima).
 __device__ __forceinline__ float max64(const f32x2 (&x)[32]) {
   float m[4], a, b;
@@ -165,6 +160,30 @@ __device__ __forceinline__ bool widen_agree(bool yes) {
 // The n lowest bits (all from 32 on, none for n <= 0).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// -inf for the keys 2 u, 2 u + 1 whose bits of see are not set.
+__device__ __forceinline__ void mask64(f32x2 (&x)[32], const uint32_t (&see)[2]) {
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    float a, b;
+    unpair2(x[u], a, b);
+    const uint32_t bits = see[u >> 4];
+    x[u] = pair2(bits & (1u << ((2 * u) & 31)) ? a : -INFINITY, bits & (1u << ((2 * u + 1) & 31)) ? b : -INFINITY);
+  }
+}
+// The largest magnitude of the others.
+__device__ __forceinline__ float max64_seen(const f32x2 (&x)[32], const uint32_t (&see)[2]) {
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    float a, b;
+    unpair2(x[u], a, b);
+    const uint32_t bits = see[u >> 4];
+    if (bits & (1u << ((2 * u) & 31))) m = fmaxf(m, fabsf(a));
+    if (bits & (1u << ((2 * u + 1) & 31))) m = fmaxf(m, fabsf(b));
+  }
+  return m;
 }
 
 // Each lane of a quad holds four 16-byte units u[0..3] of its row; afterwards lane q holds unit q of the quad's
@@ -739,9 +758,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       const float exp_in = cap_in * 2.8853900817779268f;  // 2 log2(e) / softcap, of a product
       const float slope = BIAS ? sc.slopes[h] * 1.4426950408889634f : 0.f;
       // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
-      // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers leave fp32's range.)
+      // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers overflow; one that
+      // vanishes leaves the linear term.)
       f32x2 cc[4];
-      float near2 = -1.f;  // the largest x^2 that it is for
+      float near1 = -1.f;  // the largest |x| that it is for
       if constexpr (CAP) {
         const float z2 = cap_in * cap_in;
         float c = cap_out * cap_in;
@@ -751,7 +771,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           cc[u] = pair2(c * fit[u], c * fit[u]);
           c *= z2;
         }
-        if (z2 < 1e6f && z2 > 1e-18f) near2 = 0.25f / z2;
+        if (z2 < 1e6f) near1 = z2 > 1e-37f ? 0.5f / fabsf(cap_in) : 1e18f;
       }
       // (FP8 pool: read again where they are used, to keep the 128 registers a thread for the scores: held in
       // registers they took the causal prompt of 8192 tokens from 571 to 714 us)
@@ -803,15 +823,33 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             return m_ref == -INFINITY ? 0.f : -m_ref;
           };
           float lsum;  // of the half's weights
-          bool near = false;
+          // bit t of see[i]: the row sees key 32 i + t of the half
+          auto seen = [&](uint32_t (&see)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) see[i] = low_bits(hi - th - 32 * i) & ~low_bits(lo - th - 32 * i);
+            if (blocks != all) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int b = 0; b < 32 / BS; ++b)
+                  if (!((blocks >> (hf * (NBT / 2) + i * (32 / BS) + b)) & 1u))
+                    see[i] &= ~((BS == 32 ? 0xffffffffu : (1u << (BS & 31)) - 1u) << (b * BS));
+            }
+          };
+          const bool all_whole = __all_sync(kFull, whole);
+          bool fast = false;  // the whole warp sees the whole half, and the scores take their short form
           float top = 0.f;
-          if constexpr (CAP) {
-            top = max64(x);
-            const float bottom = -max64neg(x);
-            near = __all_sync(kFull, fmaxf(top * top, bottom * bottom) <= near2);  // the warp's scores: at most half the cap
-            if (cap_in < 0.f) top = bottom;
+          if (!BIAS && all_whole) {
+            if constexpr (CAP) {
+              top = max64(x);
+              const float bottom = -max64neg(x);
+              fast = __all_sync(kFull, fmaxf(top, -bottom) <= near1);  // at most half the cap
+              if (cap_in < 0.f) top = bottom;
+            } else {
+              fast = sl2 >= 0.f;
+            }
           }
-          if (!BIAS && __all_sync(kFull, whole) && (CAP ? near : sl2 >= 0.f)) {
+          if (fast) {
             if constexpr (CAP) {
               const f32x2 t = pair2(top, top), t2 = mul2(t, t);
               float mx, unused;
@@ -829,6 +867,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             }
           } else {
             if constexpr (CAP) {
+              bool near = (BIAS || !all_whole) && __all_sync(kFull, max3(max64(x), max64neg(x), 0.f) <= near1);
+              if (!near && !all_whole) {  // (a key that is not seen may hold anything)
+                uint32_t see[2];
+                seen(see);
+                near = __all_sync(kFull, max64_seen(x, see) <= near1);
+              }
               if (near) {
 #pragma unroll
                 for (int u = 0; u < 32; ++u) {
@@ -864,26 +908,9 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
               if constexpr (BIAS) add_bias(x, slope, pos - th);
             }
             if (!whole) {
-              // bit t of see[i]: the row sees key 32 i + t of the half
               uint32_t see[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) see[i] = low_bits(hi - th - 32 * i) & ~low_bits(lo - th - 32 * i);
-              if (blocks != all) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                  for (int b = 0; b < 32 / BS; ++b)
-                    if (!((blocks >> (hf * (NBT / 2) + i * (32 / BS) + b)) & 1u))
-                      see[i] &= ~((BS == 32 ? 0xffffffffu : (1u << (BS & 31)) - 1u) << (b * BS));
-              }
-#pragma unroll
-              for (int u = 0; u < 32; ++u) {
-                float v0, v1;
-                unpair2(x[u], v0, v1);
-                const uint32_t bits = see[u >> 4];
-                x[u] = pair2(bits & (1u << ((2 * u) & 31)) ? v0 : -INFINITY,
-                             bits & (1u << ((2 * u + 1) & 31)) ? v1 : -INFINITY);
-              }
+              seen(see);
+              mask64(x, see);
             }
             const float nm = reference(max64(x));
             const f32x2 sub = pair2(nm, nm);

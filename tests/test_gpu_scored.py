@@ -100,6 +100,14 @@ def test_decode_caps(softcap, dtype):
     check(b, softcap=softcap)
 
 
+@pytest.mark.parametrize("softcap", [1e-3, 0.5, 50.0, 1e6])
+@pytest.mark.parametrize("dtype,fp8", [("f16", False), ("bf16", False), ("bf16", True)])
+def test_multi_query_caps(softcap, dtype, fp8):
+    b = R.build(15, [70, 300, 9], [70, 130, 2], 8, 2, 128, 16, dtype, fp8, spread=4.0)
+    check(b, softcap=softcap)
+    check(b, softcap=softcap, window=40, key_begin=R.documents(b, 4))
+
+
 MQ = [  # contexts, query lengths
     ([5, 40, 131, 300], [5, 4, 131, 64]),       # whole prompts and chunks
     ([1, 77, 200, 64, 9], [1, 0, 3, 64, 2]),    # one token, none, few
