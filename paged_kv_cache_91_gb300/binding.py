@@ -463,6 +463,10 @@ def paged_attention_scored_workspace_size(num_query_tokens: int, num_heads: int,
                                                             partition_size))
 
 
+# The current device's index, without torch.cuda's lazy initialisation test (a CUDA tensor exists by then).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int) -> None:
     """t must be a contiguous tensor of this type on CUDA device dev."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
@@ -483,7 +487,7 @@ def _run_on(dev: int, stream, fn, args) -> None:
         handle = _raw_stream(dev)
     else:
         handle = torch.cuda.current_stream(dev).cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -503,14 +507,16 @@ def _scored(out, query, key_cache, value_cache, block_tables, context_lens, quer
     dev = query.get_device()
     if dt is None or dev < 0 or not query.is_contiguous():
         _cuda16("query", query)
-    _expect("out", out, dtype, dev)
     if fp8:
+        _expect("out", out, dtype, dev)
         for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
             _cuda_fp8(n, t)
             _expect(n, t, t.dtype, dev)
     else:
-        _expect("key_cache", key_cache, dtype, dev)
-        _expect("value_cache", value_cache, dtype, dev)
+        for t in (out, key_cache, value_cache):
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                for n, x in (("out", out), ("key_cache", key_cache), ("value_cache", value_cache)):
+                    _expect(n, x, dtype, dev)
     _expect("block_tables", block_tables, torch.int32, dev)
     _expect("context_lens", context_lens, torch.int32, dev)
     shape, pool, tables = query.shape, key_cache.shape, block_tables.shape
@@ -562,6 +568,8 @@ def _scored(out, query, key_cache, value_cache, block_tables, context_lens, quer
                                                            partition_size)
         if wbytes:
             workspace = torch.empty(wbytes, dtype=torch.uint8, device=query.device)
+            if stream is not None:  # the allocator may hand it out again only once that stream is done with it
+                workspace.record_stream(stream)
     if workspace is not None:
         ws = workspace.data_ptr()
     scales = (k_scale, v_scale) if fp8 else ()
@@ -645,15 +653,13 @@ def _pool_arrays(block_tables, context_lens, lens_name, lens, free_blocks, num_f
     """Check the arrays that the reserve and release calls share; returns (sequences, table width, device)."""
     dev = block_tables.get_device()
     i32 = torch.int32
-    if dev < 0:
-        _cuda_i32("block_tables", block_tables)
-    _expect("block_tables", block_tables, i32, dev)
-    _expect("context_lens", context_lens, i32, dev)
-    _expect(lens_name, lens, i32, dev)
-    _expect("free_blocks", free_blocks, i32, dev)
-    _expect("num_free", num_free, i32, dev)
-    _expect("context_lens_out", context_lens_out, i32, dev)
-    _expect("num_free_out", num_free_out, i32, dev)
+    for t in (block_tables, context_lens, lens, free_blocks, num_free, context_lens_out, num_free_out):
+        if t.dtype is not i32 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            for n, x in (("block_tables", block_tables), ("context_lens", context_lens), (lens_name, lens),
+                         ("free_blocks", free_blocks), ("num_free", num_free),
+                         ("context_lens_out", context_lens_out), ("num_free_out", num_free_out)):
+                _cuda_i32(n, x)
+                _expect(n, x, i32, dev)
     tables = block_tables.shape
     if len(tables) != 2:
         raise PagedKVError(-1, "block_tables must be [S][max_blocks]")

@@ -761,12 +761,6 @@ PrefixPlan prefix_plan(int num_seqs, int group, int num_kv_heads, int block_size
 
 }  // namespace
 
-cudaError_t launch_mq_order(const int32_t* context_lens, int num_seqs, int ctx_limit, int32_t* order,
-                            cudaStream_t stream) {
-  return launch_kernel(pkv_mq_order_kernel, dim3(1), dim3(kOrderBuckets), 0, stream, context_lens, num_seqs, ctx_limit,
-                       order);
-}
-
 void set_last_error_message(const char* msg) { snprintf(g_msg, sizeof g_msg, "%s", msg); }
 
 unsigned* device_error_word(int dev) { return error_word(dev); }
@@ -1083,7 +1077,8 @@ pkv_status_t mq_impl(void* out, const void* query, const void* key_cache, const 
   if (tile != PKV_MQ_TILE_ROWS && num_seqs > 1 && workspace && aligned16(workspace) &&
       workspace_bytes >= order_at + (size_t)num_seqs * sizeof(int32_t)) {
     int32_t* order = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(workspace) + order_at);
-    e = launch_mq_order(context_lens, num_seqs, max_context_len, order, stream);
+    e = launch_kernel(pkv_mq_order_kernel, dim3(1), dim3(kOrderBuckets), 0, stream, context_lens, num_seqs,
+                      max_context_len, order);
     if (e != cudaSuccess) return cuda_fail(e, "sequence order kernel launch");
     mq.order = order;
   }

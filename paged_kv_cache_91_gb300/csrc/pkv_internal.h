@@ -86,10 +86,6 @@ bool make_pool_map(CUtensorMap* map, const void* base, long long rows, int head_
 bool make_pool_map_fp8_rows(CUtensorMap* map, const void* base, long long rows, int block_size);
 bool make_pool_map_tc(CUtensorMap* map, const void* base, long long rows, int block_size, pkv_dtype_t dtype);
 
-// The sequences by context length, longest first, into order[num_seqs].
-cudaError_t launch_mq_order(const int32_t* context_lens, int num_seqs, int ctx_limit, int32_t* order,
-                            cudaStream_t stream);
-
 // Set the calling thread's pkv_last_error_message() text.
 void set_last_error_message(const char* msg);
 // The same from a format, returning the status (cuda_fail: PKV_ERR_CUDA with the CUDA error's text).

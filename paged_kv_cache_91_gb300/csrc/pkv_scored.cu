@@ -136,11 +136,12 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if (!isfinite(c.scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
   if (!(isfinite(c.softcap) && c.softcap >= 0.f))
     return fail(PKV_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
-  if (c.softcap > 0.f && !isfinite(c.scale / c.softcap))
-    return fail(PKV_ERR_INVALID_ARG, "scale / softcap is not finite");
   if (c.window < 0) return fail(PKV_ERR_INVALID_ARG, "window must be >= 0 (0: no window)");
   if (c.fp8 && !(isfinite(c.k_scale) && isfinite(c.v_scale) && c.k_scale > 0.f && c.v_scale > 0.f))
     return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
+  const float scale = c.fp8 ? c.scale * c.k_scale : c.scale;  // of a product of the stored values
+  if (!isfinite(scale * 1.4426950408889634f) || (c.softcap > 0.f && !isfinite(scale / c.softcap)))
+    return fail(PKV_ERR_INVALID_ARG, "scale (times k_scale) or its quotient by softcap is not finite");
   if (c.fp8 && c.head_dim != 128)
     return fail(PKV_ERR_UNSUPPORTED, "scored attention over an FP8 pool needs head_dim 128 (got %d)", c.head_dim);
   if (c.max_context_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len < 0");
@@ -186,7 +187,6 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   DecodeParams p{};
   p.err = device_error_word(dev);
   if (!p.err) return fail(PKV_ERR_CUDA, "device error word unavailable on device %d", dev);
-  const float scale = c.fp8 ? c.scale * c.k_scale : c.scale;  // of a product of the stored values
   p.out = c.out;
   p.query = c.query;
   p.key_cache = static_cast<const unsigned char*>(c.key_cache);

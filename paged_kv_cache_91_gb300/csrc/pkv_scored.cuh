@@ -25,7 +25,6 @@ struct ScoreParams {
   float cap_in = 0.f;                   // scale / softcap
   float cap_out = 0.f;                  // softcap * log2(e); 0: no cap
   int row_tiles = 1;                    // row tiles per (partition, kv head, sequence)
-  const int32_t* order = nullptr;       // if set, the sequence of grid index z (longest context first)
 };
 
 __device__ __forceinline__ float fast_rcp(float x) {

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
   // the last row tiles first: with a causal limit they see the most keys
   const int part = blockIdx.x / sc.row_tiles, rt = sc.row_tiles - 1 - (int)blockIdx.x % sc.row_tiles;
   const int kvh = blockIdx.y;
-  const int s = sc.order ? sc.order[blockIdx.z] : (int)blockIdx.z;
+  const int s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, P = p.partition_size;
   const bool reporter = blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0;

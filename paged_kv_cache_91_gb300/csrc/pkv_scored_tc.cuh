@@ -272,7 +272,7 @@ __device__ __forceinline__ ScoredItem scored_item(const DecodeParams& p, const S
   m.part = x / sc.row_tiles;
   m.rt = sc.row_tiles - 1 - x % sc.row_tiles;
   m.kvh = y;
-  m.s = sc.order ? sc.order[z] : z;
+  m.s = z;
   const bool reporter = x == 0 && y == 0 && lane == 0;
   m.ctx = clamp_context(p, m.s, reporter);
   m.q0 = 0;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     prefetch_tensormap(&vmap);
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + k, F8 ? 4 : 2);
-      mbar_init(empty + k, 2);
+      mbar_init(empty + k, 2);  // the streams
       mbar_init(raw + k, 2);
     }
     for (int k = 0; k < 2; ++k) {
@@ -621,11 +621,21 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       if (m.ntile == 0) continue;
       const bool shared = shared_rows(m);
       const int first = shared ? st : 0, step = shared ? 2 : 1;
-      if (lane == 0 && first < m.ntile) {
+      if (lane == 0) {
         const uint32_t q_addr = smem_u32(smem) + (shared ? 0 : st * Sh::QT);
+        // The other stream's tile of shared rows: waited for and freed like one of this stream's. (Every waiter goes
+        // through every phase of a barrier: one that left a phase out could not tell the next from the last.)
+        auto skip_tile = [&](int j) {
+          for (int it = 2 * (tiles + j); it < 2 * (tiles + j) + 2; ++it) {
+            if (!tc_wait(full + it % NS, (it / NS) & 1, abort)) return false;
+            mbar_arrive(empty + it % NS);
+          }
+          return true;
+        };
         // S of tile j's half hf (64 keys: 8 atoms of K) into that half's columns, which the caller knows are free
         auto issue_s = [&](int j, int hf) {
           const int ik = 2 * (tiles + j);
+          if (hf == 0 && shared && j > 0 && !skip_tile(j - 1)) return false;
           if (hf == 0 && !tc_wait(full + ik % NS, (ik / NS) & 1, abort)) return false;
           tc::fence_after_sync();
           const uint32_t k_addr = smem_u32(slot(ik)) + hf * 8 * Sh::ATOM;
@@ -634,16 +644,25 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             tc::mma_f16(scol + hf * 64, tc::desc_sw128(q_addr + (u / 4) * (ROWS * 128) + (u % 4) * 32, 16, 1024),
                         tc::desc_sw128(k_addr + (u / 4) * 1024 + (u % 4) * 32, 16, Sh::ATOM), IDESC_S, u > 0);
           tc::commit(s_full + 2 * st + hf);
-          if (hf) {
-            tc::commit(empty + ik % NS);
-            if (shared) tc::commit(empty + ik % NS);  // (the other stream does not read this tile)
-          }
+          if (hf) tc::commit(empty + ik % NS);
           return true;
         };
         // a P's columns take the next S: not before its PV has read it
         auto pv_read = [&](int hf) { return cnt == 0 || tc_wait(pv_done + 2 * st + hf, (cnt - 1) & 1, abort); };
         ok = tc_wait(q_full + st, nq & 1, abort) && (!shared || tc_wait(q_full + (st ^ 1), nq & 1, abort));
-        ok = ok && pv_read(0) && issue_s(first, 0) && pv_read(1) && issue_s(first, 1);
+        if (first < m.ntile) {
+          ok = ok && pv_read(0) && issue_s(first, 0) && pv_read(1) && issue_s(first, 1);
+        } else {  // a stream without tiles goes through the motions of one
+          for (int hf = 0; ok && hf < 2; ++hf) {
+            ok = pv_read(hf);
+            tc::commit(s_full + 2 * st + hf);
+          }
+          ++cnt;
+          for (int hf = 0; ok && hf < 2; ++hf) {
+            ok = tc_wait(p_full + 2 * st + hf, (cnt - 1) & 1, abort);
+            tc::commit(pv_done + 2 * st + hf);
+          }
+        }
         for (int j = first; ok && j < m.ntile; j += step) {
           const int iv = 2 * (tiles + j) + 1;
           const uint32_t v_addr = smem_u32(slot(iv));
@@ -660,13 +679,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                              tc::desc_sw128(v_addr + (hf * 4 + u) * 2 * Sh::ATOM, 1024, Sh::ATOM), IDESC_O,
                              j > first || hf > 0 || u > 0);
             tc::commit(pv_done + 2 * st + hf);
-            if (hf) {
-              tc::commit(empty + iv % NS);
-              if (shared) tc::commit(empty + iv % NS);
-            }
+            if (hf) tc::commit(empty + iv % NS);
             if (j + step < m.ntile) ok = pv_read(hf) && issue_s(j + step, hf);
           }
         }
+        if (ok && shared && ((m.ntile - 1) & 1) != st) ok = skip_tile(m.ntile - 1);
       }
       tiles += m.ntile;
       ++nq;
@@ -889,13 +906,14 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 }
               }
               if constexpr (BIAS) add_bias(x, slope, pos - th);
-            } else if (BIAS && __all_sync(kFull, pos >= th + 63)) {
-              // keys up to the token's own position: -slope (p - j) is linear in j, four chains of steps of 8
-              const f32x2 mul = pair2(sl2, sl2), step8 = pair2(8.f * slope, 8.f * slope);
-              const float d = (float)(th - pos);
+            } else if (BIAS && (__all_sync(kFull, pos >= th + 63) || __all_sync(kFull, pos <= th))) {
+              // keys all up to the tokens' own positions, or all from them on: -slope |p - j| is linear in j, four
+              // chains of steps of 8
+              const float d = (float)(th - pos), sl = pos <= th ? -slope : slope;
+              const f32x2 mul = pair2(sl2, sl2), step8 = pair2(8.f * sl, 8.f * sl);
               f32x2 bias[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) bias[k] = pair2(slope * (d + 2 * k), slope * (d + 2 * k + 1));
+              for (int k4 = 0; k4 < 4; ++k4) bias[k4] = pair2(sl * (d + 2 * k4), sl * (d + 2 * k4 + 1));
 #pragma unroll
               for (int u = 0; u < 32; ++u) {
                 x[u] = fma2(x[u], mul, bias[u & 3]);
@@ -955,6 +973,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         }
         if (!ok) break;
       }
+      if (first >= m.ntile) {  // a stream without tiles
+        for (int hf = 0; ok && hf < 2; ++hf) {
+          ok = __all_sync(kFull, tc_wait(s_full + 2 * w + hf, cnt & 1, abort));
+          if (ok) mbar_arrive(p_full + 2 * w + hf);
+        }
+        ++cnt;
+      }
       // ---- the next item's Q: this stream's S have all been read (of shared rows: both streams', below)
       bool going = false;
       auto next_q = [&] {
@@ -966,7 +991,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       };
       if (ok && !shared) next_q();
       // ---- epilogue: O / l
-      if (ok && n > 0)
+      if (ok)
         ok = __all_sync(kFull, tc_wait(pv_done + 2 * w, (cnt - 1) & 1, abort) &&
                                    tc_wait(pv_done + 2 * w + 1, (cnt - 1) & 1, abort));
       tc::fence_after_sync();

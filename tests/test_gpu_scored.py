@@ -311,3 +311,89 @@ def test_same_inputs_give_the_same_bits(qlens):
     first = call(b, softcap=9.0, partition_size=64)
     for _ in range(3):
         assert torch.equal(call(b, softcap=9.0, partition_size=64), first)
+
+
+@pytest.mark.parametrize("qlens", [None, [3, 4], [70, 90]])
+def test_bad_tensors_are_refused(qlens):
+    """Another type, layout, device or shape of any tensor raises before anything is launched."""
+    b = R.build(34, [100, 150], qlens, 4, 2, 64, 16)
+    T = b["q"].shape[0]
+    q, kc, vc, bt = (b[k].to(DEV) for k in ("q", "kc", "vc", "tables"))
+    ok = dict(out=torch.empty_like(q), query=q, key_cache=kc, value_cache=vc, block_tables=bt,
+              context_lens=i32(b["ctx"]), scale=0.125, max_context_len=150)
+    fn = binding.paged_attention_decode_scored
+    if qlens is not None:
+        fn = binding.paged_attention_multi_query_scored
+        ok.update(query_start_loc=i32(b["starts"]), max_query_len=max(qlens))
+    fn(**ok)
+    bad = [dict(out=torch.empty_like(q).half()), dict(key_cache=kc.half()), dict(value_cache=vc[:-1]),
+           dict(query=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(query=q.cpu()), dict(out=torch.empty_like(q[:-1])),
+           dict(block_tables=bt.long()), dict(block_tables=bt[:1]), dict(context_lens=i32([1])),
+           dict(alibi_slopes=torch.ones(3, device=DEV)), dict(alibi_slopes=torch.ones(4, device=DEV).double()),
+           dict(key_begin=i32([0] * (T + 1))), dict(key_begin=torch.zeros(T, device=DEV)), dict(softcap=-1.0),
+           dict(window=-1), dict(partition_size=24), dict(max_context_len=10 ** 6),
+           dict(partition_size=16, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
+           dict(partition_size=16, workspace=torch.empty(1 << 20, dtype=torch.uint8))]
+    if qlens is not None:
+        bad += [dict(key_end=i32([0] * (T - 1))), dict(query_start_loc=i32([0, T])), dict(max_query_len=151)]
+    for kw in bad:
+        with pytest.raises(binding.PagedKVError):
+            fn(**{**ok, **kw})
+    torch.cuda.synchronize()
+    assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("qlens", [None, [70, 90]])
+def test_workspace_of_a_call_on_another_stream(qlens):
+    """A call on a side stream with a workspace of its own making, beside work on the current stream."""
+    b = R.build(35, [900, 700], qlens, 8, 2, 128, 16)
+    ref, tol = R.reference(b, softcap=6.0)
+    side = torch.cuda.Stream()
+    out = torch.full_like(b["q"], float("nan"), device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        junk = [torch.full((1 << 18,), float("nan"), device=DEV) for _ in range(4)]
+        call(b, softcap=6.0, partition_size=64, stream=side, out=out)
+        del junk
+    assert R.worst(out, ref, tol) <= 1.0
+
+
+def test_two_calls_at_once():
+    """Calls of every tile on two streams at a time give what they give alone."""
+    cases = [(R.build(36, [700, 90, 300], None, 8, 2, 128, 16), dict(window=200)),
+             (R.build(37, [300, 400], [130, 60], 8, 2, 128, 16), dict(softcap=4.0)),
+             (R.build(38, [300, 400], [130, 60], 8, 2, 128, 16, fp8=True), dict(slopes=R.slopes_of(8)))]
+    alone = [call(b, partition_size=128, **r) for b, r in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.full_like(b["q"], float("nan"), device=DEV) for b, _ in cases]
+    kept = []
+    for _ in range(3):
+        for (b, r), s, o in zip(cases, streams, outs):
+            t = [x.to(DEV) for x in (b["q"], b["kc"], b["vc"], b["tables"])] + [i32(b["ctx"]), i32(b["starts"])]
+            sl = r["slopes"].to(DEV) if "slopes" in r else None
+            kept += t + [sl]
+            torch.cuda.synchronize()
+            kw = dict(softcap=r.get("softcap", 0.0), window=r.get("window", 0), alibi_slopes=sl, partition_size=128,
+                      max_context_len=max(b["ctx"]), stream=s)
+            if b["decode"]:
+                binding.paged_attention_decode_scored(o, *t[:5], b["scale"], **kw)
+            elif b["fp8"]:
+                binding.paged_attention_multi_query_scored_fp8(o, *t[:5], t[5], b["scale"], b["k_scale"], b["v_scale"],
+                                                               max_query_len=130, **kw)
+            else:
+                binding.paged_attention_multi_query_scored(o, *t[:5], t[5], b["scale"], max_query_len=130, **kw)
+    torch.cuda.synchronize()
+    for o, a in zip(outs, alone):
+        assert torch.equal(o, a)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_work_items(fp8):
+    """More row tiles than SMs, of very different lengths, empty ones among them: a CTA takes one after the other."""
+    ctx = [40 * (i % 11) + 3 for i in range(90)]
+    qlens = [0 if i % 7 == 3 else min(n, 1 + 37 * (i % 5)) for i, n in enumerate(ctx)]
+    b = R.build(39, ctx, qlens, 16, 4, 128, 16, "bf16", fp8)
+    T = sum(qlens)
+    begin = [(t * 37) % 90 if t % 13 else 1 << 20 for t in range(T)]
+    check(b, key_begin=begin, softcap=3.0)
+    check(b, window=25, slopes=R.slopes_of(16), part=64)

@@ -276,3 +276,31 @@ def test_serving_loop(fp8, graphed):
         assert (out[n:] == 9.0).all()
         assert binding.device_errors() == 0
     assert dev["nfree"].item() == NB - sum(-(-c // B) for c in ctx)
+
+
+def test_bad_tensors_are_refused(cuda_lib):
+    """Another type, layout, device or shape of any array raises before anything is launched."""
+    def args(**kw):
+        S = 3
+        a = dict(block_tables=torch.zeros((S, 4), dtype=torch.int32, device=DEV), context_lens=i32([1] * S),
+                 new_lens=i32([1] * S), free_blocks=i32([5, 6]), num_free=i32([2]),
+                 slot_mapping=torch.zeros(8, dtype=torch.int64, device=DEV), query_start_loc=i32([0] * (S + 1)),
+                 context_lens_out=i32([0] * S), num_free_out=i32([0]), granted=i32([0] * S), block_size=16,
+                 num_blocks=8)
+        a.update(kw)
+        return a
+
+    binding.paged_kv_reserve_slots(**args())
+    wide = torch.zeros((3, 8), dtype=torch.int32, device=DEV)
+    for kw in (dict(context_lens=i32([1, 1, 1]).long()), dict(block_tables=wide[:, ::2]), dict(new_lens=i32([1, 1])),
+               dict(slot_mapping=i32([0] * 8)), dict(query_start_loc=i32([0, 0, 0])), dict(granted=i32([0, 0])),
+               dict(num_free=i32([1, 2])), dict(free_blocks=torch.zeros(2, dtype=torch.int32)),
+               dict(context_lens_out=torch.zeros(3, dtype=torch.int32)), dict(block_size=12),
+               dict(block_tables=i32([0] * 12))):
+        with pytest.raises(binding.PagedKVError):
+            binding.paged_kv_reserve_slots(**args(**kw))
+    same = i32([1, 1, 1])
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_kv_reserve_slots(**args(context_lens=same, context_lens_out=same))
+    with pytest.raises(binding.PagedKVError):
+        binding.paged_kv_reserve_slots(**args(context_lens=same, granted=same))
