@@ -570,8 +570,12 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  *   window         >= 0; 0 is no window. The token's own position counts
  *   key_begin      [num_query_tokens] int32 (decode: [num_seqs]) device memory, or NULL
  *   key_end        [num_query_tokens] int32 device memory, or NULL (multi-query)
+ *   partition_size 0 = chosen for the batch (one CTA's keys: all of them, or a
+ *                  split that fills the GPU); else a multiple of block_size in
+ *                  [block_size, 128 * block_size]
  *   workspace      paged_attention_scored_workspace_size(...) bytes, 16-byte
- *                  aligned; may be NULL when that size is 0
+ *                  aligned; may be NULL when that size is 0 (decode: num_query_tokens
+ *                  is num_seqs and max_query_len 1)
  *   *_fp8          over an E4M3 pool, k_scale and v_scale as in
  *                  paged_attention_decode_fp8; head_dim 128 only
  *
@@ -585,6 +589,7 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  * paged_attention_multi_query (a bad query_start_loc skips its sequence and
  * sets PKV_DEVERR_QUERY; a bad block id skips its tokens and sets
  * PKV_DEVERR_BLOCK_ID). Rows of out past the last sequence are not written.
+ * max_query_len at most 524280, max_context_len at most 2^30.
  */
 size_t paged_attention_scored_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
                                              int32_t head_dim, int32_t block_size, int32_t max_query_len,

@@ -61,28 +61,6 @@ __device__ __forceinline__ void copy_tile16(unsigned char* dst, const CUtensorMa
   }
 }
 
-// What a tile's fold() does with its raw products: rule(x, ta, va, tb, vb) turns the lane's four (column 0 and
-// column 1 with token ta of the tile, then with token tb) into scores in the base-2 domain, -inf where the
-// column does not see the token (va, vb: it is among the tile's valid tokens). HOLES: a column may see no token
-// of a tile, or of all tiles so far.
-// This rule scales; with CAUSAL a column also sees only tokens whose position tok_base + t is below its limit.
-template <bool CAUSAL>
-struct ScaleRule {
-  static constexpr bool HOLES = CAUSAL;
-  float sla, slb;
-  int tok_base, lim0, lim1;
-  __device__ __forceinline__ float one(int c, float x, int t, bool in) const {
-    if constexpr (CAUSAL) in = in && tok_base + t < (c ? lim1 : lim0);
-    return in ? x * (c ? slb : sla) : -INFINITY;
-  }
-  __device__ __forceinline__ void operator()(float (&x)[4], int ta, bool va, int tb, bool vb) const {
-    x[0] = one(0, x[0], ta, va);
-    x[1] = one(1, x[1], ta, va);
-    x[2] = one(0, x[2], tb, vb);
-    x[3] = one(1, x[3], tb, vb);
-  }
-};
-
 template <typename T_, int D_, int BS_>
 struct MmaTile {
   using T = T_;  // query / output type, also the cache type
@@ -137,14 +115,6 @@ struct MmaTile {
                                              const uint32_t (&qb)[KT][2], int lane, float sla, float slb,
                                              float& m0, float& m1, float& l0, float& l1, float (&acc)[KT][4],
                                              int tok_base = 0, int lim0 = 0, int lim1 = 0) {
-    fold(Ks, Vs, 0, nvalid, qb, lane, m0, m1, l0, l1, acc, ScaleRule<CAUSAL>{sla, slb, tok_base, lim0, lim1});
-  }
-
-  // The same for tokens first .. nvalid-1 with the scores of `rule` (value rows outside are zeroed).
-  template <typename Rule>
-  static __device__ __forceinline__ void fold(unsigned char* Ks, unsigned char* Vs, int first, int nvalid,
-                                              const uint32_t (&qb)[KT][2], int lane, float& m0, float& m1,
-                                              float& l0, float& l1, float (&acc)[KT][4], const Rule& rule) {
     const int mi = lane >> 3;  // which 8x8 matrix this lane addresses in ldmatrix
     const int r8 = lane & 7;   // row inside that matrix
     const int r0 = lane >> 2;  // accumulator rows r0 and r0 + 8
@@ -158,14 +128,9 @@ struct MmaTile {
       }
       __syncwarp();
     }
-    if (first > 0) {
-      for (int idx = lane; idx < first * (D / 8); idx += 32)
-        *reinterpret_cast<uint4*>(Vs + swz_offset<BS, NBOX>(idx / (D / 8), idx % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
-      __syncwarp();
-    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (c * 16 < nvalid && c * 16 + 16 > first) {
+      if (c * 16 < nvalid) {
         // scores S^T[token][head] for 16 tokens, in two accumulation chains
         float sacc[4] = {0.f, 0.f, 0.f, 0.f};
         {
@@ -186,10 +151,19 @@ struct MmaTile {
           for (int e = 0; e < 4; ++e) sacc[e] += sacc2[e];
         }
         const int ta = c * 16 + r0, tb = ta + 8;
-        const bool va = (BS >= 16 || r0 < BS) && ta < nvalid && ta >= first;
-        const bool vb = BS >= 16 && tb < nvalid && tb >= first;
-        rule(sacc, ta, va, tb, vb);
-        const float x00 = sacc[0], x01 = sacc[1], x10 = sacc[2], x11 = sacc[3];
+        const bool va = (BS >= 16 || r0 < BS) && ta < nvalid;
+        const bool vb = BS >= 16 && tb < nvalid;
+        bool va0 = va, va1 = va, vb0 = vb, vb1 = vb;
+        if constexpr (CAUSAL) {
+          va0 = va && tok_base + ta < lim0;
+          va1 = va && tok_base + ta < lim1;
+          vb0 = vb && tok_base + tb < lim0;
+          vb1 = vb && tok_base + tb < lim1;
+        }
+        const float x00 = va0 ? sacc[0] * sla : -INFINITY;
+        const float x01 = va1 ? sacc[1] * slb : -INFINITY;
+        const float x10 = vb0 ? sacc[2] * sla : -INFINITY;
+        const float x11 = vb1 ? sacc[3] * slb : -INFINITY;
         // Lazy rescaling: a column's reference m moves (and its state is rescaled) only when one of its
         // scores exceeds m by more than 8, so p = 2^(x - m) <= 2^8. Each lane tests its own scores and the
         // warp votes; the max is reduced across the lanes only when some score does exceed.

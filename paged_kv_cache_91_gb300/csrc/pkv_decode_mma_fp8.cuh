@@ -150,14 +150,6 @@ struct MmaTileE4M3 {
                                              int lane, float sla, float slb, float& m0, float& m1, float& l0,
                                              float& l1, float (&acc)[KT][4], int tok_base = 0, int lim0 = 0,
                                              int lim1 = 0) {
-    fold(Ks, Vs, 0, nvalid, qb, lane, m0, m1, l0, l1, acc, ScaleRule<CAUSAL>{sla, slb, tok_base, lim0, lim1});
-  }
-
-  // The same for tokens first .. nvalid-1 with the scores of `rule` (value rows outside are zeroed).
-  template <typename Rule>
-  static __device__ __forceinline__ void fold(unsigned char* Ks, unsigned char* Vs, int first, int nvalid,
-                                              const QB& qb, int lane, float& m0, float& m1, float& l0, float& l1,
-                                              float (&acc)[KT][4], const Rule& rule) {
     const int g = lane >> 2, qd = lane & 3;
     if (nvalid < BS) {
       // value rows past the context may hold anything (NaN codes too): zero them
@@ -167,14 +159,9 @@ struct MmaTileE4M3 {
         *reinterpret_cast<uint4*>(Vs + (nvalid + idx / 8) * 128 + (idx % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
       __syncwarp();
     }
-    if (first > 0) {
-      for (int idx = lane; idx < first * 8; idx += 32)
-        *reinterpret_cast<uint4*>(Vs + (idx / 8) * 128 + (idx % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      __syncwarp();
-    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (c * 16 < nvalid && c * 16 + 16 > first) {
+      if (c * 16 < nvalid) {
         // K rows of this lane: c*16 + g and + 8 (with BS = 8 the second aliases the first; masked)
         const int ta = c * 16 + g, tb = BS >= 16 ? ta + 8 : ta;
         const uint4 ka0 = *reinterpret_cast<const uint4*>(Ks + off(ta, 2 * qd));
@@ -197,10 +184,19 @@ struct MmaTileE4M3 {
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) sacc[e] += sacc2[e];
-        const bool va = ta < nvalid && ta >= first;
-        const bool vb = BS >= 16 && ta + 8 < nvalid && ta + 8 >= first;
-        rule(sacc, ta, va, ta + 8, vb);
-        const float x00 = sacc[0], x01 = sacc[1], x10 = sacc[2], x11 = sacc[3];
+        const bool va = ta < nvalid;
+        const bool vb = BS >= 16 && ta + 8 < nvalid;
+        bool va0 = va, va1 = va, vb0 = vb, vb1 = vb;
+        if constexpr (CAUSAL) {
+          va0 = va && tok_base + ta < lim0;
+          va1 = va && tok_base + ta < lim1;
+          vb0 = vb && tok_base + ta + 8 < lim0;
+          vb1 = vb && tok_base + ta + 8 < lim1;
+        }
+        const float x00 = va0 ? sacc[0] * sla : -INFINITY;
+        const float x01 = va1 ? sacc[1] * slb : -INFINITY;
+        const float x10 = vb0 ? sacc[2] * sla : -INFINITY;
+        const float x11 = vb1 ? sacc[3] * slb : -INFINITY;
         // Lazy rescaling: a column's reference m moves (and its state is rescaled)
         // only when a score exceeds it by more than 8, so p = 2^(x - m) <= 2^8. Each
         // lane tests its own scores and the warp votes; the max is reduced across
@@ -215,7 +211,7 @@ struct MmaTileE4M3 {
           const bool up0 = mx0 > m0 + 8.f, up1 = mx1 > m1 + 8.f;
           const float mn0 = up0 ? mx0 : m0, mn1 = up1 ? mx1 : m1;
           float al0 = fast_exp2(m0 - mn0), al1 = fast_exp2(m1 - mn1);
-          if constexpr (Rule::HOLES) {  // a column that keeps its m may still hold -inf there
+          if constexpr (CAUSAL) {  // a column that keeps its m may still hold -inf there
             if (!up0) al0 = 1.f;
             if (!up1) al1 = 1.f;
           }
@@ -232,7 +228,7 @@ struct MmaTileE4M3 {
           m1 = mn1;
         }
         float r0 = m0, r1 = m1;  // exponentials against the reference
-        if constexpr (Rule::HOLES) {  // a column that has seen nothing yet: against 0 (its x are all -inf)
+        if constexpr (CAUSAL) {  // a column that has seen nothing yet: against 0 (its x are all -inf)
           if (r0 == -INFINITY) r0 = 0.f;
           if (r1 == -INFINITY) r1 = 0.f;
         }

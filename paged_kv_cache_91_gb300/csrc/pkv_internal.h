@@ -74,9 +74,10 @@ cudaError_t scored_cols_fp8(const DecodeParams& p, const ScoreParams& sc, const 
 
 // The same on the tensor-memory tile; the pool through make_pool_map_tc (16-bit, head_dim 128), make_pool_map
 // (16-bit, head_dim 64) or make_pool_map_fp8_rows.
-cudaError_t scored_tc_16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, bool f16, int head_dim, int block_size, int num_seqs,
-                         cudaStream_t stream);
+cudaError_t scored_tc_f16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int head_dim, int block_size, int num_seqs, cudaStream_t stream);
+cudaError_t scored_tc_bf16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                           const CUtensorMap& vmap, int head_dim, int block_size, int num_seqs, cudaStream_t stream);
 cudaError_t scored_tc_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
 

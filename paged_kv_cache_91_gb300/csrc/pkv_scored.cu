@@ -238,7 +238,8 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   const bool f16 = c.dtype == PKV_F16;
   if (pl.tensor)
     e = c.fp8 ? scored_tc_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
-              : scored_tc_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
+        : f16 ? scored_tc_f16(p, sc, kmap, vmap, c.head_dim, c.block_size, c.num_seqs, c.stream)
+              : scored_tc_bf16(p, sc, kmap, vmap, c.head_dim, c.block_size, c.num_seqs, c.stream);
   else
     e = c.fp8 ? scored_cols_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
               : scored_cols_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);

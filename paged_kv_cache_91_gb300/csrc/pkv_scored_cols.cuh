@@ -1,6 +1,5 @@
 // Scored paged attention with few rows per kv head: 8 (query token, head) rows per CTA in the n = 8 dimension
-// of the warp MMAs, the CTA's warps splitting the partition's blocks (the tile of pkv_decode_mma.cuh and
-// pkv_decode_mma_fp8.cuh). Row r of a (sequence, kv head) is query token r / G, head kvh * G + r % G; decode is
+// of the warp MMAs, the CTA's warps splitting the partition's blocks (pkv_scored_tile.cuh). Row r of a (sequence, kv head) is query token r / G, head kvh * G + r % G; decode is
 // the case of one query token, with every group size, 1 included.
 //
 // A tile's products become scores in registers (ScoredRule): the tanh is two exponential-unit operations and
@@ -8,14 +7,12 @@
 // bound by the reading of K and V. Only the blocks between the CTA's first and last visible key are copied.
 #pragma once
 
-#include "pkv_decode_mma.cuh"
-#include "pkv_decode_mma_fp8.cuh"
 #include "pkv_scored.cuh"
+#include "pkv_scored_tile.cuh"
 
 namespace pkv {
 
 struct ScoredRule {
-  static constexpr bool HOLES = true;
   float mul0, mul1;      // of the raw product: scale * log2(e), or scale / softcap
   float cap_out;         // softcap * log2(e), 0: no cap
   bool biased;

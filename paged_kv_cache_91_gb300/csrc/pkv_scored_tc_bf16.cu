@@ -1,12 +1,12 @@
-// Scored paged attention on the tensor-memory tile: f16 and bf16 pools.
+// Scored paged attention on the tensor-memory tile: bf16 pools.
 #include "pkv_internal.h"
 #include "pkv_scored_tc.cuh"
 
 namespace pkv {
 
-template <typename T>
-static cudaError_t dispatch(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
-                            const CUtensorMap& vmap, int head_dim, int block_size, int num_seqs, cudaStream_t stream) {
+cudaError_t scored_tc_bf16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int head_dim, int block_size, int num_seqs, cudaStream_t stream) {
+  using T = __nv_bfloat16;
   if (head_dim == 128) {
     if (block_size == 16) return launch_scored_tc<T, 128, 16, false>(p, sc, kmap, vmap, num_seqs, stream);
     if (block_size == 8) return launch_scored_tc<T, 128, 8, false>(p, sc, kmap, vmap, num_seqs, stream);
@@ -17,13 +17,6 @@ static cudaError_t dispatch(const DecodeParams& p, const ScoreParams& sc, const 
     if (block_size == 32) return launch_scored_tc<T, 64, 32, false>(p, sc, kmap, vmap, num_seqs, stream);
   }
   return cudaErrorInvalidValue;
-}
-
-cudaError_t scored_tc_16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, bool f16, int head_dim, int block_size, int num_seqs,
-                         cudaStream_t stream) {
-  return f16 ? dispatch<__half>(p, sc, kmap, vmap, head_dim, block_size, num_seqs, stream)
-             : dispatch<__nv_bfloat16>(p, sc, kmap, vmap, head_dim, block_size, num_seqs, stream);
 }
 
 }  // namespace pkv
