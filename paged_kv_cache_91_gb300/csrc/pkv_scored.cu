@@ -66,7 +66,8 @@ long long scored_span_bound(int block_size, int max_query_len, int max_context_l
 }
 
 ScoredPlan scored_plan(int num_query_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                       int max_query_len, int max_context_len, int window, int partition_size) {
+                       int max_query_len, int max_context_len, int window, int partition_size,
+                       size_t workspace_bytes = SIZE_MAX) {
   ScoredPlan pl{};
   const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
   pl.tensor = rows >= kScoredTensorRows;
@@ -84,7 +85,12 @@ ScoredPlan scored_plan(int num_query_tokens, int num_heads, int num_kv_heads, in
     long long n = pl.tensor ? 1 : span > p0 ? (span + p0 / 2) / p0 : 1;
     const long long fill = ctas > 0 ? ((pl.tensor ? kScoredFillTensor : kScoredFill) + ctas - 1) / ctas : 1;
     const long long most = span / (pl.tensor ? kScoredMinTensor : kScoredMin);
-    if (n < fill) n = fill < most ? fill : (n < most ? most : n);
+    // (as far as the workspace goes: one that fits a larger batch fits a smaller one, which is split further)
+    const size_t one = (size_t)num_query_tokens * num_heads * (head_dim + 2) * sizeof(float);
+    const long long room = one ? (long long)(workspace_bytes / one < (1u << 30) ? workspace_bytes / one : 1u << 30) : 1;
+    long long more = fill < most ? fill : most;
+    if (more > room) more = room;
+    if (n < more) n = more;
     long long P = ((span + n - 1) / n + block_size - 1) / block_size * block_size;
     if (!pl.tensor && P > (long long)kMaxPartitionBlocks * block_size) P = (long long)kMaxPartitionBlocks * block_size;
     pl.P = P < block_size ? block_size : (int)P;
@@ -165,7 +171,8 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if ((long long)c.num_query_tokens * c.num_heads >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "num_query_tokens * num_heads must be < 2^31");
   const ScoredPlan pl = scored_plan(c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
-                                    c.max_query_len, c.max_context_len, c.window, c.partition_size);
+                                    c.max_query_len, c.max_context_len, c.window, c.partition_size,
+                                    c.workspace ? c.workspace_bytes : 0);
   if ((long long)pl.np * pl.row_tiles >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "partitions * row tiles must be < 2^31");
   if (c.num_seqs == 0 || c.num_query_tokens == 0 || c.max_query_len == 0) return PKV_OK;

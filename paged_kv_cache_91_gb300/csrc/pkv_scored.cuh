@@ -109,46 +109,102 @@ __device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned cha
   }
 }
 
-// One row over the keys [a, b) on one warp, key by key, its lanes holding D / 32 dims each: (m, l) and the
-// output normalised by l. The tiles multiply every key of a tile with every row, a masked one with weight 0,
-// and 0 times a NaN or infinite value is NaN: a tile's row that comes out non-finite is computed again here,
-// where a masked key is not touched. So only batches that hold such values pay for it.
+// One row over the keys [a, b) on one warp: (m, l) and the output normalised by l. Lane t scores key t of 32, then
+// the lanes hold D / 32 dims each for their weighted values. The tiles multiply every key of a tile with every row,
+// a masked one with weight 0, and 0 times a NaN or infinite value is NaN: a row that such a value may have reached
+// is computed again here, where a masked key is not touched.
 template <typename T, typename C, int D>
 __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams& sc, size_t row, int s, int h,
                                         int pos, int a, int b, int block_size, int lane, float& m, float& l,
                                         float (&o)[D / 32]) {
-  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB;
+  constexpr int DPL = D / 32, EB = CacheFmt<C>::EB, EPP = 16 / EB;
   const int g = h / p.group;
   const float slope = sc.slopes ? sc.slopes[h] * 1.4426950408889634f : 0.f;
-  float q[DPL];
-  load_dims<D, T>(q, static_cast<const unsigned char*>(p.query) + row * D * 2, lane);
+  const unsigned char* q = static_cast<const unsigned char*>(p.query) + row * D * 2;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) o[e] = 0.f;
   m = -INFINITY;
   l = 0.f;
-  for (int j = a; j < b; ++j) {
-    const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];
-    if ((unsigned)phys >= (unsigned)p.num_blocks) continue;  // (reported by the tile)
-    const size_t at = (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB;
-    float k[DPL], v[DPL], d = 0.f;
-    load_dims<D, C>(k, p.key_cache + at, lane);
-    load_dims<D, C>(v, p.value_cache + at, lane);
+  for (int j0 = a; j0 < b; j0 += 32) {
+    const int j = j0 + lane;
+    const int phys = j < b ? p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size] : -1;
+    const bool ok = (unsigned)phys < (unsigned)p.num_blocks;  // (a bad id is reported by the tile)
+    const size_t at = ok ? (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB : 0;
+    float d = 0.f;
+    if (ok) {
+#pragma unroll 4
+      for (int c = 0; c < D / EPP; ++c) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(p.key_cache + at + c * 16);
+        const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) d = fmaf(q[e], k[e], d);
-    d = warp_sum(d);
-    const float x = (sc.cap_out != 0.f ? sc.cap_out * score_tanh(d * sc.cap_in) : d * p.scale_log2) -
-                    slope * fabsf((float)(pos - j));
-    const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = fast_exp2(m - ms), w = fast_exp2(x - ms);
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) o[e] = fmaf(o[e], f, w * v[e]);
+        for (int e = 0; e < EPP / 2; ++e) {
+          const float2 kf = CacheFmt<C>::pair(EB == 1 ? kw[e / 2] >> (16 * (e & 1)) : kw[e & 3]);
+          const float2 qf = Elem<T>::to_float2(*reinterpret_cast<const uint32_t*>(q + (c * EPP + 2 * e) * 2));
+          d = fmaf(qf.x, kf.x, d);
+          d = fmaf(qf.y, kf.y, d);
+        }
+      }
+    }
+    const float x = ok ? (sc.cap_out != 0.f ? sc.cap_out * score_tanh(d * sc.cap_in) : d * p.scale_log2) -
+                             slope * fabsf((float)(pos - j))
+                       : -INFINITY;
+    const float mn = fmaxf(m, warp_max(x)), ms = mn == -INFINITY ? 0.f : mn;
+    const float f = fast_exp2(m - ms), w = ok ? fast_exp2(x - ms) : 0.f;
+    l = fmaf(l, f, warp_sum(w));
     m = mn;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) o[e] *= f;
+    const unsigned in = __ballot_sync(kFull, ok);
+#pragma unroll 4
+    for (int t = 0; t < 32; ++t) {
+      const float wt = __shfl_sync(kFull, w, t);
+      const size_t vt = __shfl_sync(kFull, (unsigned long long)at, t);
+      if ((in >> t) & 1u) {
+        float v[DPL];
+        load_dims<D, C>(v, p.value_cache + vt, lane);
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) o[e] = fmaf(wt, v[e], o[e]);
+      }
+    }
   }
   const float inv = l != 0.f ? p.v_scale / l : 0.f;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) o[e] *= inv;
   if (l != l) m = 0.f;  // (a partial with m = -inf would be left out of the merge)
+}
+
+// The first and the last key of [a, b) whose value row of kv head g holds a NaN or an infinity (first > last: none),
+// on one warp.
+template <typename C, int D>
+__device__ __noinline__ void bad_values(const DecodeParams& p, int s, int g, int a, int b, int block_size, int lane,
+                                        int& first, int& last) {
+  constexpr int EB = CacheFmt<C>::EB, CH = D * EB / 16, KPI = 32 / CH;  // pieces of a row, keys per load
+  first = INT32_MAX;
+  last = -1;
+#pragma unroll 4
+  for (int j0 = a; j0 < b; j0 += KPI) {
+    const int j = j0 + lane / CH;
+    if (j >= b) continue;
+    const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];
+    if ((unsigned)phys >= (unsigned)p.num_blocks) continue;
+    const uint4 v4 = *reinterpret_cast<const uint4*>(
+        p.value_cache + (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB + lane % CH * 16);
+    const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < 2 / EB; ++k) {
+        const float2 f = CacheFmt<C>::pair(v[e] >> (16 * k));
+        bad = bad || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+      }
+    if (bad) {
+      first = min(first, j);
+      last = max(last, j);
+    }
+  }
+  first = __reduce_min_sync(kFull, first);
+  last = __reduce_max_sync(kFull, last);
 }
 
 // The row's result of one partition: the output itself, or its partial.

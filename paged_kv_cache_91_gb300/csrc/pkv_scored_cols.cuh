@@ -277,7 +277,9 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
     }
     const int r = row0 + n, h = kvh * G + r % G;
     const size_t row = (size_t)(q0 + r / G) * p.num_heads + h;
-    if (!__all_sync(kFull, fine))
+    // a non-finite row is a masked key's doing only if it misses some of the keys that the CTA multiplies, and not if
+    // its own scores are NaN
+    if (!__all_sync(kFull, fine) && L == L && (nlo > c0 || nhi < c1))
       scored_row<T, C, D>(p, sc, row, s, h, ctx - q_len + r / G, max(nlo, tok0), min(nhi, tok0 + P), BS, lane, M, L, o);
     store_row<T, D>(p, row, part, np.direct(), lane, M, L, o);
   }

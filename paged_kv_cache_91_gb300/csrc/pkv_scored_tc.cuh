@@ -1063,8 +1063,15 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           p.part_m[(size_t)orow * p.max_partitions + m.part] = ok ? m_ref : -INFINITY;
           p.part_l[(size_t)orow * p.max_partitions + m.part] = ok ? l : 0.f;
         }
-        // rows that came out non-finite: again, key by key, on the whole warp
-        for (uint32_t redo = __ballot_sync(kFull, mine && !fine); redo; redo &= redo - 1) {
+        // Rows that came out non-finite by a masked key's value (not by NaN scores of their own): again, on the whole
+        // warp. A value that every such row sees is theirs, so a NaN in the cache costs one look over the item's values.
+        uint32_t redo = __ballot_sync(kFull, mine && !fine && ok && l == l && (lo > m.c0 || hi < m.c1));
+        if (redo) {
+          int bad0, bad1;
+          bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1);
+          redo &= __ballot_sync(kFull, bad0 > bad1 || lo > bad0 || hi <= bad1);
+        }
+        for (; redo; redo &= redo - 1) {
           const int src = __ffs(redo) - 1;
           const int rlo = __shfl_sync(kFull, lo, src), rhi = __shfl_sync(kFull, hi, src);
           const int rpos = __shfl_sync(kFull, pos, src), rh = __shfl_sync(kFull, h, src);

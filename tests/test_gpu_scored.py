@@ -51,6 +51,7 @@ SHAPES = [  # H, Hkv, D, B, dtype, fp8
     (4, 4, 64, 16, "f16", False), (8, 2, 128, 16, "bf16", False), (6, 2, 64, 8, "bf16", False),
     (8, 8, 128, 32, "f16", False), (16, 1, 128, 8, "f16", False), (20, 4, 128, 16, "bf16", False),
     (8, 1, 128, 16, "bf16", True), (4, 4, 128, 8, "f16", True), (24, 2, 128, 32, "bf16", True),
+    (20, 1, 128, 16, "f16", False), (33, 1, 64, 8, "bf16", False), (40, 2, 128, 32, "bf16", True),
 ]
 RULES = ["none", "cap", "alibi", "window", "begin", "all"]
 
@@ -397,3 +398,55 @@ def test_many_work_items(fp8):
     begin = [(t * 37) % 90 if t % 13 else 1 << 20 for t in range(T)]
     check(b, key_begin=begin, softcap=3.0)
     check(b, window=25, slopes=R.slopes_of(16), part=64)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("where", [[5], [5, 700], [300, 301]])
+def test_a_nan_in_a_long_prompt(where, fp8):
+    """A NaN value row reaches the tokens that see it, from its position on, and no earlier one."""
+    n = 800
+    b = R.build(40, [n], [n], 4, 1, 128, 16, "bf16", fp8)
+    for j in where:
+        b["vc"][b["tables"][0, j // 16], :, j % 16] = 0x7F if fp8 else float("nan")
+    out = call(b, softcap=5.0).double().cpu()
+    clean = dict(b, qlens=[where[0]], ctx=[where[0]], q=b["q"][:where[0]])
+    ref, tol = R.reference(clean, softcap=5.0)
+    assert R.worst(out[:where[0]], ref, tol) <= 1.0
+    assert torch.isnan(out[where[0]:]).all()
+
+
+def test_one_bad_value_in_many_tiles_costs_little():
+    """4096 tokens that all see a NaN key keep to the tile: no row is computed again for a value that is its own."""
+    n, H, Hkv, D, B = 4096, 16, 4, 128, 16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kc, vc = (torch.randn((n // B, Hkv, B, D), device=DEV, dtype=torch.bfloat16, generator=g) for _ in range(2))
+    q = torch.randn((n, H, D), device=DEV, dtype=torch.bfloat16, generator=g)
+    tables = torch.arange(n // B, device=DEV, dtype=torch.int32)[None].contiguous()
+    out = torch.empty_like(q)
+    times = []
+    for bad in (False, True):
+        if bad:
+            vc[0, :, 0] = float("nan")
+        for _ in range(2):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            binding.paged_attention_multi_query_scored(out, q, kc, vc, tables, i32([n]), i32([0, n]), 0.1, softcap=9.0,
+                                                       max_query_len=n, max_context_len=n)
+            end.record()
+            torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert torch.isnan(out).all()
+    assert times[1] < 100 * times[0] + 50.0  # (key by key it would be thousands of times)
+
+
+def test_a_workspace_for_more_fits_less():
+    """A workspace sized for a larger batch serves every smaller one, however that is split."""
+    kw = dict(num_heads=8, num_kv_heads=2, head_dim=128, block_size=16, max_query_len=1, max_context_len=6000)
+    big = binding.paged_attention_scored_workspace_size(7, **kw)
+    ws = torch.empty(max(big, 16), dtype=torch.uint8, device=DEV)
+    for S in range(1, 8):
+        b = R.build(41 + S, [6000 - 777 * i for i in range(S)], None, 8, 2, 128, 16)
+        ref, tol = R.reference(b, softcap=5.0)
+        out = call(b, softcap=5.0, workspace=ws, max_ctx=6000)
+        assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
