@@ -7,11 +7,11 @@ namespace pkv {
 template <typename T>
 static cudaError_t dispatch(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                             const CUtensorMap& vmap, int block_size, int num_seqs, cudaStream_t stream) {
-  constexpr int R = PKV_MMA_FP8_RING_BYTES;
+  constexpr int R = PKV_MMA_FP8_RING_BYTES, D = 128;
   using C = __nv_fp8_e4m3;
-  if (block_size == 16) return launch_scored_cols<ScoredTileE4M3<T, 128, 16>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
-  if (block_size == 8) return launch_scored_cols<ScoredTileE4M3<T, 128, 8>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
-  if (block_size == 32) return launch_scored_cols<ScoredTileE4M3<T, 128, 32>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
+  if (block_size == 16) return launch_scored_cols<ScoredTileE4M3<T, D, 16>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
+  if (block_size == 8) return launch_scored_cols<ScoredTileE4M3<T, D, 8>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
+  if (block_size == 32) return launch_scored_cols<ScoredTileE4M3<T, D, 32>, C, R>(p, sc, kmap, vmap, num_seqs, stream);
   return cudaErrorInvalidValue;
 }
 

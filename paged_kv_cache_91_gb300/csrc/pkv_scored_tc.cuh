@@ -13,11 +13,12 @@
 // threads exponentiate. A CTA with at most 128 rows gives both streams the same rows: stream w then takes every
 // second tile, and their (m, l, O) are merged at the end.
 //
-// What bounds it: per 256 x 128 scores the tensor cores need about 2048 cycles (head_dim 128) and the shared
-// memory port as many (Q and K twice, V twice, the copies once); the exponentials take 1 special-function
-// operation a score and the scores 4 to 8 fp32 operations (cap), which is of the same size. So the streams
-// overlap the two, and a score is kept to few instructions: tiles that every row sees whole skip the masks,
-// and the tanh is a polynomial where the tile's scores stay well below the cap.
+// What bounds it: per 256 x 128 scores the tensor cores need about 2048 cycles (head_dim 128), the shared memory
+// port 2500 (Q for every half, K and V for both streams, the copies once) and the exponentials 1024; measured are
+// 3500 without and 4300 with a cap (1170 and 980 TFLOP/s of visible scores, a causal prompt of 8192 tokens, 32/8
+// heads), with no unit saturated: it is the chain from S to P in the row threads. So a score is kept to few
+// instructions: tiles that every row sees whole skip the masks, the tanh is a polynomial where the tile's scores
+// stay well below the cap, and both are computed on pairs.
 //
 // A CTA stays and takes one (partition, row tile, kv head, sequence) after the other: when its copies of an item
 // are issued it asks the hardware for the next unstarted CTA of the grid and does that one's work too. So the
@@ -725,8 +726,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       const bool shared = shared_rows(i);
       unsigned char* Qs = smem + (shared ? 0 : w * Sh::QT);
       if constexpr (Q_AS_F16)  // (both streams need the factors of shared rows)
-        qscale_next = scored_fetch_q_bf16_as_f16<ROWS>(Qs, warp & 3, lane, reinterpret_cast<const __nv_bfloat16*>(p.query),
-                                                       own, !shared || w == 0);
+        qscale_next = scored_fetch_q_bf16_as_f16<ROWS>(
+            Qs, warp & 3, lane, reinterpret_cast<const __nv_bfloat16*>(p.query), own, !shared || w == 0);
       else if (!shared || w == 0)
         scored_fetch_q<T, D, ROWS>(Qs, warp & 3, lane, reinterpret_cast<const T*>(p.query), own);
     };
@@ -810,7 +811,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         const uint32_t blocks = __ballot_sync(kFull, next) & all;
         if (j + step < ntile()) next = load_ok(j + step);
         const int tb = c0() / BS * BS + j * NT;  // position of the tile's first token
-        const bool edge = blocks != all || tb < c0() || tb + NT > c1();  // V rows outside the item's keys, or not copied
+        // V rows outside the item's keys, or not copied
+        const bool edge = blocks != all || tb < c0() || tb + NT > c1();
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           const int th = tb + hf * 64;
@@ -902,7 +904,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                   float v0, v1;
                   unpair2(mul2(x[u], pair2(exp_in, exp_in)), v0, v1);
                   unpair2(add2(pair2(fast_exp2(v0), fast_exp2(v1)), pair2(1.f, 1.f)), v0, v1);
-                  x[u] = fma2(pair2(fast_rcp(v0), fast_rcp(v1)), pair2(-2.f * cap_out, -2.f * cap_out), pair2(cap_out, cap_out));
+                  x[u] = fma2(pair2(fast_rcp(v0), fast_rcp(v1)), pair2(-2.f * cap_out, -2.f * cap_out),
+                              pair2(cap_out, cap_out));
                 }
               }
               if constexpr (BIAS) add_bias(x, slope, pos - th);
@@ -1063,8 +1066,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           p.part_m[(size_t)orow * p.max_partitions + m.part] = ok ? m_ref : -INFINITY;
           p.part_l[(size_t)orow * p.max_partitions + m.part] = ok ? l : 0.f;
         }
-        // Rows that came out non-finite by a masked key's value (not by NaN scores of their own): again, on the whole
-        // warp. A value that every such row sees is theirs, so a NaN in the cache costs one look over the item's values.
+        // Rows that came out non-finite by a masked key's value (not by NaN scores of their own): again, on the
+        // whole warp. A value that a row sees is its own, so a NaN in the cache costs one look over the item's values.
         uint32_t redo = __ballot_sync(kFull, mine && !fine && ok && l == l && (lo > m.c0 || hi < m.c1));
         if (redo) {
           int bad0, bad1;

@@ -244,7 +244,8 @@ def test_contexts_are_clamped_and_reported():
 def test_bad_query_offsets_skip_their_sequence(q):
     b = R.build(29, [60, 70, 80], [q, q, q], 8, 2, 128, 16)
     ref, tol = R.reference(b, softcap=5.0)
-    for starts, good in (([0, q, q - 1, 3 * q], [0]), ([0, q, 2 * q, 3 * q + 1], [0, 1]), ([-1, q, 2 * q, 3 * q], [1, 2])):
+    for starts, good in (([0, q, q - 1, 3 * q], [0]), ([0, q, 2 * q, 3 * q + 1], [0, 1]),
+                         ([-1, q, 2 * q, 3 * q], [1, 2])):
         # ([0, q, q - 1, 3q]: sequence 1 has a negative length, sequence 2 more tokens than max_query_len)
         out = call(dict(b, starts=starts), softcap=5.0)
         for s in range(3):
@@ -328,7 +329,8 @@ def test_bad_tensors_are_refused(qlens):
         ok.update(query_start_loc=i32(b["starts"]), max_query_len=max(qlens))
     fn(**ok)
     bad = [dict(out=torch.empty_like(q).half()), dict(key_cache=kc.half()), dict(value_cache=vc[:-1]),
-           dict(query=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(query=q.cpu()), dict(out=torch.empty_like(q[:-1])),
+           dict(query=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(query=q.cpu()),
+           dict(out=torch.empty_like(q[:-1])),
            dict(block_tables=bt.long()), dict(block_tables=bt[:1]), dict(context_lens=i32([1])),
            dict(alibi_slopes=torch.ones(3, device=DEV)), dict(alibi_slopes=torch.ones(4, device=DEV).double()),
            dict(key_begin=i32([0] * (T + 1))), dict(key_begin=torch.zeros(T, device=DEV)), dict(softcap=-1.0),

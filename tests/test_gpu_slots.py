@@ -241,7 +241,8 @@ def test_serving_loop(fp8, graphed):
         with torch.cuda.graph(graph):
             step()
     hist = [dict(k=[], v=[]) for _ in range(S)]
-    for new, gone in (([33, 7, 0], [0, 0, 0]), ([1, 1, 12], [0, 0, 0]), ([1, 40, 1], [0, 1, 0]), ([1, 1, 1], [0, 0, 0])):
+    for new, gone in (([33, 7, 0], [0, 0, 0]), ([1, 1, 12], [0, 0, 0]), ([1, 40, 1], [0, 1, 0]),
+                      ([1, 1, 1], [0, 0, 0])):
         n = sum(new)
         hq, hk, hv = (torch.randn((T, h, D), generator=g).to(dt) for h in (H, Hkv, Hkv))
         for dst, src in ((q, hq), (k, hk), (v, hv)):
