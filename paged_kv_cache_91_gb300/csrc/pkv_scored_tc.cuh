@@ -131,8 +131,8 @@ struct ScoredTcShape {
   static constexpr int OFF_RING = 2 * QT;
   static constexpr int OFF_BARS = OFF_RING + NS * TILE;
   // barriers: full[8], empty[8], raw[8] per slot; per stream q_full, fin; per stream and half s_full, p_full,
-  // pv_done; items: info_full[2], info_empty[2], next
-  static constexpr int NBARS = 24 + 16 + 5;
+  // pv_done; items: info_full[2], info_empty[2], next; q_shared
+  static constexpr int NBARS = 24 + 16 + 6;
   static constexpr int OFF_NEXT = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;  // the hardware's answer: the next CTA
   static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag
   static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   uint64_t* info_full = bars + 40;   // [2]
   uint64_t* info_empty = bars + 42;  // [2]
   uint64_t* next_bar = bars + 44;
+  uint64_t* q_shared = bars + 45;  // shared rows' Q, which stream 0 brings
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert(sizeof(ScoredItem) <= 64, "an item's place");
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       mbar_init(info_empty + k, Sh::THREADS / 32 - 1);  // every warp but the one that finds the items
     }
     mbar_init(next_bar, 1);
+    mbar_init(q_shared, ROWS);
     fence_mbar_init();
     *abort = 0;
   }
@@ -622,6 +624,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     const uint32_t scol = tbase + Sh::S_COL + st * NT, ocol = tbase + Sh::O_COL + st * 128;
     ScoredItem m;
     int tiles = 0, cnt = 0, nq = 0;  // ring tiles of the items before, this stream's tiles, items with keys
+    int nshared = 0;                 // of them with shared rows
     bool ok = true;
     for (int k = 0; ok; ++k) {
       ok = read_item(k, m);
@@ -659,7 +662,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         };
         // a P's columns take the next S: not before its PV has read it
         auto pv_read = [&](int hf) { return cnt == 0 || tc_wait(pv_done + 2 * st + hf, (cnt - 1) & 1, abort); };
-        ok = tc_wait(q_full + st, nq & 1, abort) && (!shared || tc_wait(q_full + (st ^ 1), nq & 1, abort));
+        // Shared rows are stream 0's to bring, so stream 1 waits for those too, on a barrier of shared items alone:
+        // of q_full[0] it would leave out the other items' phases, and in those the streams may be an item apart.
+        ok = tc_wait(q_full + st, nq & 1, abort) &&
+             (st == 0 || !shared || tc_wait(q_shared, nshared++ & 1, abort));
         if (first > 0) ok = ok && skip_tile(0);
         if (first < m.ntile) {
           ok = ok && pv_read(0) && issue_s(first, 0) && pv_read(1) && issue_s(first, 1);
@@ -740,15 +746,16 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       else if (!shared || w == 0)
         scored_fetch_q<T, D, ROWS>(Qs, warp & 3, lane, reinterpret_cast<const T*>(p.query), own);
     };
-    auto finish_q = [&] {
+    auto finish_q = [&](const ScoredItem& i) {
       cp_async_wait_all();
       fence_proxy_async_smem();  // generic-proxy writes, read by the S MMAs
       mbar_arrive(q_full + w);
+      if (w == 0 && shared_rows(i)) mbar_arrive(q_shared);
     };
     bool ok = rows_agree(wait_item(0));
     if (ok && info(0)->ntile > 0) {
       start_q(*info(0));
-      finish_q();
+      finish_q(*info(0));
     }
     for (int k = 0; ok; ++k) {
       const ScoredItem& m = *info(k);
@@ -775,7 +782,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         ok = rows_agree(wait_item(k + 1));
         if (ok && info(k + 1)->ntile > 0) {
           start_q(*info(k + 1));
-          finish_q();
+          finish_q(*info(k + 1));
         }
         continue;
       }
@@ -998,7 +1005,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         going = wait_item(k + 1);
         if (going && info(k + 1)->ntile > 0) {
           start_q(*info(k + 1));
-          if (Q_AS_F16) finish_q();
+          if (Q_AS_F16) finish_q(*info(k + 1));
         }
       };
       if (ok && !shared) next_q();
@@ -1028,7 +1035,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         }
       }
       if (ok && shared) next_q();
-      if (!Q_AS_F16 && going && info(k + 1)->ntile > 0) finish_q();
+      if (!Q_AS_F16 && going && info(k + 1)->ntile > 0) finish_q(*info(k + 1));
       if (!shared || w == 0) {
         const bool mine = active && parts.in(m.part), direct = parts.direct();
         // 1 / l (FP8 pool: times the value of one V code)

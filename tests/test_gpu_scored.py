@@ -452,3 +452,20 @@ def test_a_workspace_for_more_fits_less():
         out = call(b, softcap=5.0, workspace=ws, max_ctx=6000)
         assert R.worst(out, ref, tol) <= 1.0
     assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,D,dtype", [(16, 1, 128, "bf16"), (16, 2, 64, "f16")])
+def test_rows_shared_by_the_streams_after_a_short_item(H, Hkv, D, dtype):
+    """Row tiles of more than 128 rows and one tile of keys, first of their CTA, and then row tiles of few rows and
+    many keys: the second stream may reach the latter before the first stream's queries of the former are there."""
+    G = H // Hkv
+    first, then = 320 // Hkv, 320 // Hkv  # more than two items an SM
+    q_len = [-(-(129 + 13 * (i % 9)) // G) for i in range(first)] + [1 + i % (128 // G) for i in range(then)]
+    q_len[-1] = 256 // G  # (row tiles of 256 rows for the batch)
+    ctx = [max(q_len[i], 20 + i % 90) for i in range(first)] + [140 + 50 * (i % 7) for i in range(then)]
+    b = R.build(60, ctx, q_len, H, Hkv, D, 16, dtype)
+    ref, tol = R.reference(b, softcap=5.0)
+    outs = [call(b, softcap=5.0) for _ in range(8)]
+    assert R.worst(outs[0], ref, tol) <= 1.0
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    assert binding.device_errors() == 0
