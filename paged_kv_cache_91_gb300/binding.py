@@ -126,6 +126,16 @@ def _stream(t: torch.Tensor, stream):
     return stream.cuda_stream
 
 
+def _new_workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A workspace for one call on `stream` (None: the current one), from the memory that the allocator keeps for that
+    stream: memory freed on another one may still be in use by work queued there, and is given out again only in the
+    order of its own stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def _cuda16(name: str, t: torch.Tensor) -> int:
     dt = _DTYPE.get(t.dtype)
     if dt is None or not t.is_cuda or not t.is_contiguous():
@@ -229,7 +239,7 @@ def paged_attention_decode(out: torch.Tensor, query: torch.Tensor, key_cache: to
     if workspace is None:  # (a workspace passed in is checked against the size by the library)
         need = int(lib.paged_attention_workspace_size(S, H, Hkv, D, B, max_context_len, partition_size))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            workspace = _new_workspace(need, query, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib, lib.paged_attention_decode(
         _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), maxb,
@@ -291,7 +301,7 @@ def paged_attention_decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache
     if workspace is None:
         need = int(lib.paged_attention_workspace_size_fp8(S, H, Hkv, D, B, max_context_len, partition_size))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            workspace = _new_workspace(need, query, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib, lib.paged_attention_decode_fp8(
         _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), maxb,
@@ -349,7 +359,7 @@ def _multi_query(out, query, key_cache, value_cache, block_tables, context_lens,
         need = int(lib.paged_attention_multi_query_workspace_size(T, H, Hkv, D, B, max_context_len,
                                                                   partition_size))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            workspace = _new_workspace(need, query, stream)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     head = (_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables), maxb,
             _ptr(context_lens), _ptr(query_start_loc), S, T, int(max_query_len), int(max_context_len), float(scale),
@@ -420,7 +430,7 @@ def _shared_prefix(out, query, key_cache, value_cache, prefix_blocks, prefix_len
         max_tail_len = maxb * B
     if workspace is None:
         need = paged_attention_shared_prefix_workspace_size(S, H, Hkv, D, B, int(prefix_len), int(max_tail_len))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=query.device)
+        workspace = _new_workspace(max(need, 16), query, stream)
     wbytes = workspace.numel() * workspace.element_size()
     head = (_ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(prefix_blocks), int(prefix_len),
             _ptr(block_tables), maxb, _ptr(tail_lens), S, int(max_tail_len), float(scale), B, H, Hkv, D, NB, dt)
@@ -567,9 +577,7 @@ def _scored(out, query, key_cache, value_cache, block_tables, context_lens, quer
         wbytes = lib.paged_attention_scored_workspace_size(T, H, Hkv, D, B, max_query_len, max_context_len, window,
                                                            partition_size)
         if wbytes:
-            workspace = torch.empty(wbytes, dtype=torch.uint8, device=query.device)
-            if stream is not None:  # the allocator may hand it out again only once that stream is done with it
-                workspace.record_stream(stream)
+            workspace = _new_workspace(wbytes, query, stream)
     if workspace is not None:
         ws = workspace.data_ptr()
     scales = (k_scale, v_scale) if fp8 else ()

@@ -155,3 +155,26 @@ def test_binding_refuses_cpu_tensors(lib):
                                        torch.zeros(3, dtype=torch.int32), i.clone(), one.clone(), i.clone(), 16, 4)
     with pytest.raises(binding.PagedKVError):
         binding.paged_kv_release_blocks(t, i, i, i, one, i.clone(), one.clone(), 16, 4)
+
+
+def test_workspace_is_allocated_on_the_calls_stream(monkeypatch):
+    """The workspace that a call makes is taken while the call's stream is the current one."""
+    import contextlib
+
+    from paged_kv_cache_91_gb300 import binding
+
+    now = ["current"]
+
+    @contextlib.contextmanager
+    def stream_context(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    made, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (made.append(now[0]), empty(*a, **kw))[1])
+    like = torch.zeros(1)
+    assert binding._new_workspace(48, like, "side").shape == (48,)
+    assert binding._new_workspace(32, like, None).dtype is torch.uint8
+    assert made == ["side", "current"] and now == ["current"]
