@@ -658,10 +658,11 @@ pkv_status_t paged_attention_multi_query_scored_fp8(
  *   context_lens, new_lens, context_lens_out, granted   [num_seqs] int32
  *   free_blocks      [free_capacity] int32;  num_free, num_free_out  [1] int32
  *   slot_mapping     [max_tokens] int64;  query_start_loc  [num_seqs + 1] int32
- * All in device memory. The *_out arrays and granted must not overlap the
- * inputs (PKV_ERR_INVALID_ARG). The call reads its inputs only, apart from the
- * new table entries, so that repeating it with the same inputs gives the same
- * result. The blocks of a table are its sequence's alone: shared blocks
+ * All in device memory. The arrays that the call writes (block_tables,
+ * slot_mapping, query_start_loc, the *_out arrays and granted) must not overlap
+ * one another or the inputs (PKV_ERR_INVALID_ARG). The call reads its inputs
+ * only, apart from the new table entries, so that repeating it with the same
+ * inputs gives the same result. The blocks of a table are its sequence's alone: shared blocks
  * (copy-on-write) are the host BlockPool's.
  *
  * Device-side checks: a negative length, or n + k > max_blocks_per_seq * B,
@@ -692,7 +693,7 @@ pkv_status_t paged_kv_reserve_slots(int32_t* block_tables, int32_t max_blocks_pe
  * keep their entries (a context of 0 says that they are stale).
  *
  * Shapes, overlap rule and limits as in paged_kv_reserve_slots; free_blocks is
- * updated in place. Device-side checks: a context outside [0,
+ * updated in place, so that it is written here and block_tables read. Device-side checks: a context outside [0,
  * max_blocks_per_seq * B] is clamped and sets PKV_DEVERR_CONTEXT; a table entry
  * outside [0, num_blocks) is pushed as -1 and sets PKV_DEVERR_BLOCK_ID (a
  * reserve refuses to hand it out); blocks past free_capacity are not written

@@ -687,7 +687,7 @@ def paged_kv_reserve_slots(block_tables: torch.Tensor, context_lens: torch.Tenso
     """Slots for new_lens[s] more tokens of each sequence, with blocks from the top of the free stack
     free_blocks[:num_free]: updates block_tables in place and writes slot_mapping [max_tokens] int64 (-1: padding,
     or a sequence that got nothing), query_start_loc [S + 1], context_lens_out [S], num_free_out [1] and granted [S].
-    The outputs must not overlap the inputs."""
+    What is written must not overlap anything else of the call."""
     lib = _lib or load()
     S, maxb, dev = _pool_arrays(block_tables, context_lens, "new_lens", new_lens, free_blocks, num_free,
                                 context_lens_out, num_free_out)
@@ -707,7 +707,7 @@ def paged_kv_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tens
                             free_blocks: torch.Tensor, num_free: torch.Tensor, context_lens_out: torch.Tensor,
                             num_free_out: torch.Tensor, block_size: int, num_blocks: int, stream=None) -> None:
     """Push the blocks of the sequences with finished[s] != 0 on the free stack free_blocks (in place), and write
-    context_lens_out [S] (0 for them) and num_free_out [1]. The outputs must not overlap the inputs."""
+    context_lens_out [S] (0 for them) and num_free_out [1]. What is written must not overlap anything else of the call."""
     lib = _lib or load()
     S, maxb, dev = _pool_arrays(block_tables, context_lens, "finished", finished, free_blocks, num_free,
                                 context_lens_out, num_free_out)

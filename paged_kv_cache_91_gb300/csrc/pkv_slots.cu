@@ -250,9 +250,28 @@ __global__ void __launch_bounds__(kSlotThreads) pkv_release_blocks_kernel(const 
     p.num_free_out[0] = (int)min(nfree + total.a + total.b, (long long)p.free_capacity);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
+// A device array of a call. (A null or empty one overlaps nothing.)
+struct Span {
+  const char* name;
+  const void* at;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// Every CTA reads the inputs for itself while others write: an array that is written shares no byte with another one
+// of the call, read or written.
+template <int NW, int NR>
+pkv_status_t check_apart(const Span (&written)[NW], const Span (&read)[NR]) {
+  for (int i = 0; i < NW; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j]))
+        return fail(PKV_ERR_INVALID_ARG, "%s must not overlap %s", written[i].name, written[j].name);
+    for (const Span& in : read)
+      if (overlap(written[i], in)) return fail(PKV_ERR_INVALID_ARG, "%s must not overlap %s", written[i].name, in.name);
+  }
+  return PKV_OK;
 }
 
 // The checks that both calls share. (An empty batch launches too: its totals are outputs.)
@@ -292,10 +311,18 @@ pkv_status_t paged_kv_reserve_slots(int32_t* block_tables, int32_t max_blocks_pe
       (num_seqs > 0 && (!block_tables || !context_lens || !new_lens || !context_lens_out || !granted)))
     return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   const size_t n = (size_t)num_seqs * sizeof(int32_t);
-  if (overlap(context_lens_out, n, context_lens, n) || overlap(context_lens_out, n, new_lens, n) ||
-      overlap(granted, n, context_lens, n) || overlap(granted, n, new_lens, n) ||
-      overlap(num_free_out, sizeof(int32_t), num_free, sizeof(int32_t)))
-    return fail(PKV_ERR_INVALID_ARG, "context_lens_out, granted and num_free_out must not overlap the inputs");
+  const Span written[] = {{"block_tables", block_tables, n * (size_t)max_blocks_per_seq},
+                          {"slot_mapping", slot_mapping, (size_t)max_tokens * sizeof(int64_t)},
+                          {"query_start_loc", query_start_loc, n + sizeof(int32_t)},
+                          {"context_lens_out", context_lens_out, n},
+                          {"num_free_out", num_free_out, sizeof(int32_t)},
+                          {"granted", granted, n}};
+  const Span read[] = {{"context_lens", context_lens, n},
+                       {"new_lens", new_lens, n},
+                       {"free_blocks", free_blocks, (size_t)free_capacity * sizeof(int32_t)},
+                       {"num_free", num_free, sizeof(int32_t)}};
+  const pkv_status_t apart = check_apart(written, read);
+  if (apart != PKV_OK) return apart;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -336,9 +363,15 @@ pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_bl
       (num_seqs > 0 && (!block_tables || !context_lens || !finished || !context_lens_out)))
     return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   const size_t n = (size_t)num_seqs * sizeof(int32_t);
-  if (overlap(context_lens_out, n, context_lens, n) || overlap(context_lens_out, n, finished, n) ||
-      overlap(num_free_out, sizeof(int32_t), num_free, sizeof(int32_t)))
-    return fail(PKV_ERR_INVALID_ARG, "context_lens_out and num_free_out must not overlap the inputs");
+  const Span written[] = {{"free_blocks", free_blocks, (size_t)free_capacity * sizeof(int32_t)},
+                          {"context_lens_out", context_lens_out, n},
+                          {"num_free_out", num_free_out, sizeof(int32_t)}};
+  const Span read[] = {{"block_tables", block_tables, n * (size_t)max_blocks_per_seq},
+                       {"context_lens", context_lens, n},
+                       {"finished", finished, n},
+                       {"num_free", num_free, sizeof(int32_t)}};
+  const pkv_status_t apart = check_apart(written, read);
+  if (apart != PKV_OK) return apart;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");

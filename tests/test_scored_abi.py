@@ -178,3 +178,44 @@ def test_workspace_is_allocated_on_the_calls_stream(monkeypatch):
     assert binding._new_workspace(48, like, "side").shape == (48,)
     assert binding._new_workspace(32, like, None).dtype is torch.uint8
     assert made == ["side", "current"] and now == ["current"]
+
+
+# Bytes of each array of a call of 3 sequences, tables of 8 entries, 4 free blocks and 9 tokens.
+RESERVE_WRITES = dict(block_tables=96, slot_mapping=72, query_start_loc=16, context_lens_out=12, num_free_out=4, granted=12)
+RESERVE_READS = dict(context_lens=12, new_lens=12, free_blocks=16, num_free=4)
+RELEASE_WRITES = dict(free_blocks=16, context_lens_out=12, num_free_out=4)
+RELEASE_READS = dict(block_tables=96, context_lens=12, finished=12, num_free=4)
+
+
+@pytest.mark.parametrize("call,writes,reads", [(reserve, RESERVE_WRITES, RESERVE_READS),
+                                               (release, RELEASE_WRITES, RELEASE_READS)])
+def test_what_is_written_overlaps_nothing(lib, call, writes, reads):
+    """An array that is written, laid over the last or the first bytes of any other one, is refused."""
+    sizes = {**writes, **reads}
+    for w in writes:
+        for other, n in sizes.items():
+            if other == w:
+                continue
+            at = 0x10000 * 99
+            step = 8 if w == "slot_mapping" else 4  # one element
+            for over in ((at + n - 1) // step * step, at - sizes[w] + step):
+                assert call(lib, **{w: P(over), other: P(at)}) == INVALID, (w, other)
+                message = lib.pkv_last_error_message().decode()
+                assert "overlap" in message and w in message and other in message
+
+
+def test_arrays_side_by_side_are_not_refused_as_overlapping(lib):
+    """Neighbours in one allocation, with nothing between them, and empty arrays at another one's address, pass the
+    check (a call without a place for its totals is refused for that alone)."""
+    at, a = 0x20000, {}
+    for name, n in {**RESERVE_WRITES, **RESERVE_READS}.items():
+        if name == "slot_mapping":
+            at = (at + 7) // 8 * 8
+        a[name] = P(at)
+        at += n
+    assert reserve(lib, **a, block_size=12) == UNSUPPORTED
+    none = dict(a, num_seqs=0, free_capacity=0, max_tokens=0, block_tables=None, slot_mapping=None, granted=a["num_free"],
+                context_lens=a["num_free"], free_blocks=a["num_free_out"])
+    for kw in (a, none):
+        reserve(lib, **kw)  # (refused for want of a device here, if at all)
+        assert b"overlap" not in lib.pkv_last_error_message()
