@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kSlotThreads) pkv_reserve_slots_kernel(const R
 #pragma unroll
     for (int k = 0; k < kSlotItems; ++k) {
       const int i = tid * kSlotItems + k, s = s0 + i;
-      const bool over = at.a + add[k] > p.max_tokens;
+      const bool over = add[k] > 0 && at.a + add[k] > p.max_tokens;  // (no tokens: none past max_tokens)
       const bool ok = !bad[k] && !over && (need[k] == 0 || at.b + need[k] <= nfree);
       s_start[i] = (int)min(at.a, (long long)p.max_tokens);
       s_ctx[i] = ctx[k];

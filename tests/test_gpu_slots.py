@@ -122,6 +122,15 @@ def test_reserve_reports_too_many_tokens():
     assert binding.device_errors() == 16
 
 
+def test_reserve_grants_a_sequence_without_tokens_behind_the_last_place():
+    """Only a sequence with tokens past max_tokens is refused: one that asks for none needs none."""
+    tables, free = [[0, -1], [1, -1], [2, -1], [3, -1]], [4, 5, 6, 7]
+    got = reserve(tables, [16, 10, 5, 0], [1, 4, 0, 0], free, 4, 16, 4, 8)
+    assert got[1] == [7 * 16, -1, -1, -1] and got[2] == [0, 1, 4, 4, 4]
+    assert got[3] == [17, 10, 5, 0] and got[4] == [3] and got[5] == [1, 0, 1, 1]
+    assert binding.device_errors() == 16
+
+
 def test_reserve_reports_bad_ids():
     got = reserve([[0, -1], [9, -1], [-1, -1]], [16, 5, 3], [1, 1, 1], [1, 2, 77], 3, 16, 3, 8)
     assert got[0] == [[0, -1], [9, -1], [-1, -1]] and got[1] == [-1, -1, -1]
