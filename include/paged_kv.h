@@ -654,6 +654,16 @@ pkv_status_t paged_attention_multi_query_scored_fp8(
  *     num_free_out[0] = num_free[0] - blocks handed out
  * and slot_mapping entries past the last token are -1.
  *
+ * A sequence that is not granted keeps its query tokens, so that the batch's
+ * layout does not depend on the grants. An attention call over
+ * context_lens_out would place them inside its old context, or find more query
+ * tokens than context (PKV_DEVERR_QUERY). Without reading granted on the host:
+ * pass paged_attention_multi_query_scored the contexts context_lens[s] +
+ * new_lens[s], and a key_begin of 2^31 - 1 for each query token whose slot is
+ * -1 (any other start for the rest). Those rows are then zeros, of their
+ * sequence no table entry is read, and no error is set. The attention calls
+ * without key_begin want granted read first, or enough free blocks.
+ *
  *   block_tables     [num_seqs][max_blocks_per_seq] int32, updated in place
  *   context_lens, new_lens, context_lens_out, granted   [num_seqs] int32
  *   free_blocks      [free_capacity] int32;  num_free, num_free_out  [1] int32

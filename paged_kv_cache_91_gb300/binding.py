@@ -687,7 +687,11 @@ def paged_kv_reserve_slots(block_tables: torch.Tensor, context_lens: torch.Tenso
     """Slots for new_lens[s] more tokens of each sequence, with blocks from the top of the free stack
     free_blocks[:num_free]: updates block_tables in place and writes slot_mapping [max_tokens] int64 (-1: padding,
     or a sequence that got nothing), query_start_loc [S + 1], context_lens_out [S], num_free_out [1] and granted [S].
-    What is written must not overlap anything else of the call."""
+    What is written must not overlap anything else of the call.
+
+    A sequence that got nothing keeps its query tokens and its context. For the scored attention calls, pass the
+    contexts context_lens + new_lens and a key_begin of 2**31 - 1 for the query tokens whose slot is -1: their rows
+    are zeros, and granted need not be read on the host before the step's end."""
     lib = _lib or load()
     S, maxb, dev = _pool_arrays(block_tables, context_lens, "new_lens", new_lens, free_blocks, num_free,
                                 context_lens_out, num_free_out)

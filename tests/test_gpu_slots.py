@@ -288,6 +288,113 @@ def test_serving_loop(fp8, graphed):
     assert dev["nfree"].item() == NB - sum(-(-c // B) for c in ctx)
 
 
+# New tokens and releases of each step, over pools of 3 and 6 blocks of 16 tokens.
+WAITING = {
+    # up to 2 query tokens a step: the tile of few rows
+    "few": (3, 3, 2, [([2, 2, 0], [0, 0, 0])] * 8 + [([1, 1, 1], [0, 0, 0]), ([1, 1, 2], [0, 0, 0]),
+                      ([2, 1, 1], [1, 0, 0]), ([1, 1, 2], [0, 1, 0])], 5),
+    "many": (6, 4, 40, [([40, 30, 0], [0, 0, 0]), ([8, 1, 20], [0, 0, 0]), ([10, 10, 1], [0, 0, 0]),
+                        ([1, 20, 40], [0, 0, 0]), ([40, 20, 1], [1, 0, 0]), ([1, 1, 16], [0, 0, 0])], 7),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("graphed", [False, True])
+@pytest.mark.parametrize("rows", ["few", "many"])
+def test_serving_loop_with_sequences_that_wait(fp8, graphed, rows):
+    """The pool runs short: a prompt, and later a sequence at the end of its last block, wait until another one is
+    released. Their query tokens have slot -1 and see no key: their rows are zeros, every other sequence's are those
+    of the definition, and no error is reported; nothing is read on the host."""
+    S, H, Hkv, D, B, T = 3, 8, 2, 128, 16, 96
+    NB, width, longest, steps, waiting = WAITING[rows]
+    scale, cap, window, ks, vs = D ** -0.5, 4.0, 30, 0.02, 0.015
+    g = torch.Generator().manual_seed(9)
+    dt = torch.bfloat16
+    kc, vc = (torch.zeros((NB, Hkv, B, D), dtype=torch.uint8 if fp8 else dt, device=DEV) for _ in range(2))
+    dev = {n: i32([0] * S) for n in ("ctx", "new", "gone", "ctx2", "granted", "ctx3", "attend")}
+    dev.update(tables=torch.full((S, width), -1, dtype=torch.int32, device=DEV), free=i32(list(range(NB))),
+               nfree=i32([NB]), nfree2=i32([0]), nfree3=i32([0]), starts=i32([0] * (S + 1)),
+               slots=torch.zeros(T, dtype=torch.int64, device=DEV), begin=i32([0] * T))
+    q = torch.zeros((T, H, D), dtype=dt, device=DEV)
+    kn, vn = (torch.zeros((T, Hkv, D), dtype=dt, device=DEV) for _ in range(2))
+    out = torch.zeros_like(q)
+
+    def step():
+        binding.paged_kv_release_blocks(dev["tables"], dev["ctx"], dev["gone"], dev["free"], dev["nfree"],
+                                        dev["ctx2"], dev["nfree2"], B, NB)
+        binding.paged_kv_reserve_slots(dev["tables"], dev["ctx2"], dev["new"], dev["free"], dev["nfree2"],
+                                       dev["slots"], dev["starts"], dev["ctx3"], dev["nfree3"], dev["granted"], B, NB)
+        torch.add(dev["ctx2"], dev["new"], out=dev["attend"])
+        torch.mul(dev["slots"] < 0, (1 << 31) - 1, out=dev["begin"])
+        args = (out, q, kc, vc, dev["tables"], dev["attend"], dev["starts"], scale)
+        kw = dict(softcap=cap, window=window, key_begin=dev["begin"], max_query_len=longest, max_context_len=width * B)
+        if fp8:
+            binding.paged_kv_write_fp8(kn, vn, kc, vc, dev["slots"], ks, vs)
+            binding.paged_attention_multi_query_scored_fp8(*args, k_scale=ks, v_scale=vs, **kw)
+        else:
+            binding.paged_kv_write(kn, vn, kc, vc, dev["slots"])
+            binding.paged_attention_multi_query_scored(*args, **kw)
+        dev["ctx"].copy_(dev["ctx3"])
+        dev["nfree"].copy_(dev["nfree3"])
+
+    graph = None
+    if graphed:
+        step()  # an empty step
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    hist, waits = [dict(k=[], v=[]) for _ in range(S)], 0
+    free = NB
+    for new, gone in steps:
+        n = sum(new)
+        hq, hk, hv = (torch.randn((T, h, D), generator=g).to(dt) for h in (H, Hkv, Hkv))
+        for dst, src in ((q, hq), (kn, hk), (vn, hv)):
+            dst.copy_(src)
+        dev["new"].copy_(i32(new))
+        dev["gone"].copy_(i32(gone))
+        out.fill_(9.0)
+        graph.replay() if graph else step()
+        torch.cuda.synchronize()
+        at, need, granted = 0, 0, []
+        for s in range(S):
+            if gone[s]:
+                free += -(-len(hist[s]["k"]) // B)
+                hist[s] = dict(k=[], v=[])
+        for s in range(S):
+            have = len(hist[s]["k"])
+            blocks = -(-(have + new[s]) // B) - -(-have // B)
+            need += blocks
+            granted.append(int(blocks == 0 or need <= free))
+            if granted[s]:
+                hist[s]["k"] += list(hk[at:at + new[s]])
+                hist[s]["v"] += list(hv[at:at + new[s]])
+            at += new[s]
+        free = NB - sum(-(-len(h["k"]) // B) for h in hist)
+        waits += granted.count(0)
+        ctx = [len(h["k"]) for h in hist]
+        assert dev["granted"].tolist() == granted and dev["ctx3"].tolist() == ctx and dev["nfree"].item() == free
+        # the definition, over the sequences that were granted
+        b = R.build(1, ctx, [x if w else 0 for x, w in zip(new, granted)], H, Hkv, D, B, "bf16", fp8)
+        if fp8:
+            b.update(k_scale=ks, v_scale=vs)
+        for s in range(S):
+            for j in range(ctx[s]):
+                for pool, name, sc in (("kc", "k", ks), ("vc", "v", vs)):
+                    x = hist[s][name][j]
+                    if fp8:
+                        x = (x.float() / sc).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                    b[pool][b["tables"][s, j // B], :, j % B] = x
+        starts = [sum(new[:s]) for s in range(S + 1)]
+        mine = [t for s in range(S) if granted[s] for t in range(starts[s], starts[s + 1])]
+        others = [t for t in range(n) if t not in mine]
+        b["q"] = hq[mine]
+        ref, tol = R.reference(b, softcap=cap, window=window)
+        assert R.worst(out[mine], ref, tol) <= 1.0
+        assert (out[others] == 0).all() and (out[n:] == 9.0).all()
+        assert binding.device_errors() == 0
+    assert waits == waiting
+
+
 def test_bad_tensors_are_refused(cuda_lib):
     """Another type, layout, device or shape of any array raises before anything is launched."""
     def args(**kw):
