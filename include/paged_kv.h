@@ -581,10 +581,13 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  *
  * Block-table entries whose tokens no query token of the sequence sees are not
  * read, so that the blocks behind a window may have been given to others, and
- * K and V rows outside a query token's interval never change its result,
- * whatever they hold. A tanh, an exponential and every sum are computed in
- * fp32; the softmax weights are rounded to the MMA's 16-bit type for their
- * product with V. Every other argument, the dtypes, the error word and the
+ * K and V rows outside a query token's interval never enter its result,
+ * whatever they hold. (Scores of other rows choose between forms of the tanh
+ * that are equally exact, and a row next to a NaN or infinite value that it
+ * does not see is computed in another order: within the roundings named here.)
+ * A tanh, an exponential and every sum are computed in fp32, a tanh to a
+ * relative 1e-6; the softmax weights are rounded to the MMA's 16-bit type for
+ * their product with V. Every other argument, the dtypes, the error word and the
  * treatment of bad inputs are those of paged_attention_decode and
  * paged_attention_multi_query (a bad query_start_loc skips its sequence and
  * sets PKV_DEVERR_QUERY; a bad block id skips its tokens and sets

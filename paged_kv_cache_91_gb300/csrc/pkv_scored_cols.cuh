@@ -50,10 +50,16 @@ struct ScoredRule {
           const float q = fmaf(u, fmaf(u, fmaf(u, -0.0444022226f, 0.131902965f), -0.333263179f), 0.999999456f);
           x[e] = cap_out * (x[e] * q);
         }
-      } else {  // some score is of the cap's size: the cancellation of 1 - 2 / (e^(2 z) + 1) is small beside it
+      } else {
+        // some score is of the cap's size: the cancellation of 1 - 2 / (e^(2 z) + 1) is small beside it, but not beside
+        // a small score, which keeps to the polynomial whatever stands beside it
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = cap_out - 2.f * cap_out * fast_rcp(fast_exp2(x[e] * 2.8853900817779268f) + 1.f);
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[e] * x[e];
+          const float q = fmaf(u, fmaf(u, fmaf(u, -0.0444022226f, 0.131902965f), -0.333263179f), 0.999999456f);
+          const float far = cap_out - 2.f * cap_out * fast_rcp(fast_exp2(x[e] * 2.8853900817779268f) + 1.f);
+          x[e] = fabsf(x[e]) <= 0.5f ? cap_out * (x[e] * q) : far;
+        }
       }
     }
     if (biased) {

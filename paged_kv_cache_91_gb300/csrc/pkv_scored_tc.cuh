@@ -789,7 +789,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       const int first = shared ? w : 0, step = shared ? 2 : 1;
       const float sl2 = p.scale_log2 * qscale;
       const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
-      const float exp_in = cap_in * 2.8853900817779268f;  // 2 log2(e) / softcap, of a product
       const float slope = BIAS ? sc.slopes[h] * 1.4426950408889634f : 0.f;
       // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
       // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers overflow; one that
@@ -916,12 +915,23 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 }
               } else {
 #pragma unroll
-                for (int u = 0; u < 32; ++u) {  // cap_out (1 - 2 / (e^(2 z) + 1)): some score is of the cap's size
-                  float v0, v1;
-                  unpair2(mul2(x[u], pair2(exp_in, exp_in)), v0, v1);
+                for (int u = 0; u < 32; ++u) {
+                  // Some score is of the cap's size: cap_out (1 - 2 / (e^(2 z) + 1)) for those, whose cancellation is
+                  // small beside them, and the polynomial for the others, whatever stands beside them.
+                  const f32x2 z = mul2(x[u], pair2(cap_in, cap_in)), sq = mul2(z, z);
+                  f32x2 t = pair2(-0.0444022226f, -0.0444022226f);
+                  t = fma2(sq, t, pair2(0.131902965f, 0.131902965f));
+                  t = fma2(sq, t, pair2(-0.333263179f, -0.333263179f));
+                  t = fma2(sq, t, pair2(0.999999456f, 0.999999456f));
+                  float z0, z1, v0, v1, n0, n1;
+                  unpair2(z, z0, z1);
+                  unpair2(mul2(mul2(z, t), pair2(cap_out, cap_out)), n0, n1);
+                  unpair2(mul2(z, pair2(2.8853900817779268f, 2.8853900817779268f)), v0, v1);  // e^(2z) = 2^v
                   unpair2(add2(pair2(fast_exp2(v0), fast_exp2(v1)), pair2(1.f, 1.f)), v0, v1);
-                  x[u] = fma2(pair2(fast_rcp(v0), fast_rcp(v1)), pair2(-2.f * cap_out, -2.f * cap_out),
-                              pair2(cap_out, cap_out));
+                  unpair2(fma2(pair2(fast_rcp(v0), fast_rcp(v1)), pair2(-2.f * cap_out, -2.f * cap_out),
+                               pair2(cap_out, cap_out)),
+                          v0, v1);
+                  x[u] = pair2(fabsf(z0) <= 0.5f ? n0 : v0, fabsf(z1) <= 0.5f ? n1 : v1);
                 }
               }
               if constexpr (BIAS) add_bias(x, slope, pos - th);

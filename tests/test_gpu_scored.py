@@ -469,3 +469,21 @@ def test_rows_shared_by_the_streams_after_a_short_item(H, Hkv, D, dtype):
     assert R.worst(outs[0], ref, tol) <= 1.0
     assert all(torch.equal(o, outs[0]) for o in outs)
     assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("qlens", [None, [2], [40]])
+@pytest.mark.parametrize("dtype,fp8", [("f16", False), ("bf16", False), ("f16", True)])
+def test_a_score_beyond_half_the_cap_leaves_the_others_alone(dtype, fp8, qlens):
+    """A cap far above most scores, and a query head whose scores reach it, beside heads with ordinary ones in the same
+    tile: each score is as exact as it would be alone."""
+    b = R.build(62, [13 if qlens is None else qlens[0] + 12], qlens, 8, 1, 128, 16, dtype, fp8)
+    cap = 3e5
+    phys = b["tables"][0, 0]
+    key = R.values(b, b["kc"], b["k_scale"])[phys, 0, 5]
+    b["q"][:, 3] = (6e4 * key.sign()).to(b["dtype"])
+    assert (b["q"][0, 3].double() @ key) * b["scale"] > 0.6 * cap
+    ref, tol = R.reference(b, softcap=cap)
+    out = call(b, softcap=cap)
+    rest = [h for h in range(8) if h != 3]
+    assert R.worst(out[:, rest], ref[:, rest], tol[:, rest]) <= 1.0
+    assert R.worst(out, ref, tol) <= 1.0
