@@ -791,20 +791,24 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       const float cap_in = sc.cap_in * qscale, cap_out = sc.cap_out;
       const float slope = BIAS ? sc.slopes[h] * 1.4426950408889634f : 0.f;
       // cap_out * tanh(x * cap_in) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) while |x * cap_in| <= 1/2: a minimax fit of
-      // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. (Not for factors whose powers overflow; one that
-      // vanishes leaves the linear term.)
+      // tanh(z) / z in z^2 on [0, 1/4], relative error 6e-7. The coefficients hold cap_in's powers, up to the seventh:
+      // not for factors with which those come near the ends of fp32's range (caps far from the scale), whose tiles
+      // take the long form. A bf16 query over an FP8 pool, whose cap_in has the row's 2^-k, would always be such a
+      // one: there x is the product times cap_in, and the coefficients are cap_out's alone (a causal prompt of 8192
+      // tokens, cap 50: 770 us; 750 with coefficients that vanished).
+      const float unit = Q_AS_F16 ? 1.f : cap_in;  // of x, in tanh's argument
       f32x2 cc[4];
       float near1 = -1.f;  // the largest |x| that it is for
       if constexpr (CAP) {
-        const float z2 = cap_in * cap_in;
-        float c = cap_out * cap_in;
+        const float z2 = unit * unit, c3 = fabsf(cap_out * unit) * z2 * z2 * z2;
+        float c = cap_out * unit;
         const float fit[4] = {0.999999456f, -0.333263179f, 0.131902965f, -0.0444022226f};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           cc[u] = pair2(c * fit[u], c * fit[u]);
           c *= z2;
         }
-        if (z2 < 1e6f) near1 = z2 > 1e-37f ? 0.5f / fabsf(cap_in) : 1e18f;
+        if (Q_AS_F16 || (c3 > 1e-36f && c3 < 1e30f)) near1 = 0.5f / fabsf(unit);
       }
       // (FP8 pool: read again where they are used, to keep the 128 registers a thread for the scores: held in
       // registers they took the causal prompt of 8192 tokens from 571 to 714 us)
@@ -843,6 +847,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll
           for (int u = 0; u < 32; ++u)
             x[u] = pair2(__uint_as_float(sr[u >> 4][(2 * u) & 31]), __uint_as_float(sr[u >> 4][(2 * u + 1) & 31]));
+          if constexpr (CAP && Q_AS_F16) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], pair2(cap_in, cap_in));
+          }
           const bool whole = !edge && th >= lo && th + 64 <= hi;
           float f = 1.f;      // factor of what the row holds
           bool resc = false;  // O's row holds terms to rescale
@@ -878,7 +886,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
               top = max64(x);
               const float bottom = -max64neg(x);
               fast = __all_sync(kFull, fmaxf(top, -bottom) <= near1);  // at most half the cap
-              if (cap_in < 0.f) top = bottom;
+              if (unit < 0.f) top = bottom;
             } else {
               fast = sl2 >= 0.f;
             }
@@ -918,7 +926,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 for (int u = 0; u < 32; ++u) {
                   // Some score is of the cap's size: cap_out (1 - 2 / (e^(2 z) + 1)) for those, whose cancellation is
                   // small beside them, and the polynomial for the others, whatever stands beside them.
-                  const f32x2 z = mul2(x[u], pair2(cap_in, cap_in)), sq = mul2(z, z);
+                  const f32x2 z = Q_AS_F16 ? x[u] : mul2(x[u], pair2(unit, unit)), sq = mul2(z, z);
                   f32x2 t = pair2(-0.0444022226f, -0.0444022226f);
                   t = fma2(sq, t, pair2(0.131902965f, 0.131902965f));
                   t = fma2(sq, t, pair2(-0.333263179f, -0.333263179f));

@@ -487,3 +487,70 @@ def test_a_score_beyond_half_the_cap_leaves_the_others_alone(dtype, fp8, qlens):
     rest = [h for h in range(8) if h != 3]
     assert R.worst(out[:, rest], ref[:, rest], tol[:, rest]) <= 1.0
     assert R.worst(out, ref, tol) <= 1.0
+
+
+def capped_pair(cap, dtype, fp8, z):
+    """Two tiles of keys, of which two score z times the cap for every query, with values 1 and -1, so that each row is
+    0; beside the second one stands a key beyond half the cap, which leaves its half of the tile to the exponential
+    form of the tanh, while the first one's takes the polynomial. A score off by d in one of them moves a row by d / 2."""
+    n, ql, H, D = 256, 40, 8, 128
+    b = R.build(61, [n], [ql], H, 1, D, 16, dtype, fp8)
+    b.update(k_scale=0.015 if fp8 else 1.0, v_scale=2.0 ** -6 if fp8 else 1.0)
+    per = 8.0 * 128 * b["scale"] * b["k_scale"] / cap  # z of a key of ones
+    b["q"] = torch.full_like(b["q"], 8.0)
+
+    def stored(x):
+        return torch.tensor(float(x)).to(torch.float8_e4m3fn if fp8 else b["dtype"]).view(torch.uint8 if fp8 else b["dtype"])
+
+    b["kc"][:], b["vc"][:] = stored(0.0), stored(0.0)
+    for j, at, v in ((10, z, 1.0), (74, z, -1.0), (80, -0.6, 0.0)):
+        phys = b["tables"][0, j // 16]
+        b["kc"][phys, :, j % 16] = stored(at / per)
+        b["vc"][phys, :, j % 16] = stored(v / b["v_scale"])
+    k = R.values(b, b["kc"], b["k_scale"])[b["tables"][0, 0], 0, 10, 0].item()
+    assert 0.4 < 8.0 * 128 * b["scale"] * k / cap <= 0.5  # (as it is stored)
+    return b
+
+
+@pytest.mark.parametrize("cap", [20.0, 30.0, 50.0, 1000.0])
+@pytest.mark.parametrize("dtype,fp8", [("bf16", True), ("f16", True), ("bf16", False), ("f16", False)])
+def test_scores_near_half_the_cap(dtype, fp8, cap):
+    check(capped_pair(cap, dtype, fp8, 0.48), softcap=cap)
+
+
+@pytest.mark.parametrize("cap", [20.0, 30.0, 50.0])
+@pytest.mark.parametrize("dtype,fp8", [("bf16", True), ("f16", True), ("bf16", False)])
+def test_scores_near_half_the_cap_against_a_distance_bias(dtype, fp8, cap):
+    """A far key near half the cap and the keys around each token, level with it by the distance bias."""
+    b = capped_pair(cap, dtype, fp8, 0.48)
+    top = cap * 0.446  # tanh(0.48)
+    b["kc"][b["tables"][0, 4:6].long()] = 0  # (the second key and its neighbour)
+    b["vc"][:] = 0xE8 if fp8 else -1.0  # (E4M3 codes of -64 and 64, times 2^-6)
+    b["vc"][b["tables"][0, 0], :, 10] = 0x68 if fp8 else 1.0
+    slopes = torch.tensor([(top - 2.3) / 225 * (1 + 0.02 * (h - 4)) for h in range(8)], dtype=torch.float32)
+    check(b, softcap=cap, slopes=slopes)
+
+
+@pytest.mark.parametrize("cap", [3e4, 2e5, 1e6, 1e12, 1e30])
+@pytest.mark.parametrize("dtype,fp8", [("bf16", True), ("f16", True), ("bf16", False), ("f16", False)])
+def test_caps_far_above_the_scale(dtype, fp8, cap):
+    """Caps whose powers over the scale leave fp32's range, and half of which no score (of a 16-bit pool: one) reaches."""
+    if cap < 1e5 and not fp8:
+        check(capped_pair(cap, dtype, fp8, 0.48), softcap=cap)
+    for qlens in (None, [40]):
+        check(R.build(63, [256], qlens, 8, 1, 128, 16, dtype, fp8, spread=8.0), softcap=cap)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 1e3, -0.1, 0.0])
+@pytest.mark.parametrize("dtype,fp8", [("bf16", True), ("f16", True), ("f16", False)])
+def test_scales_far_from_the_cap(dtype, fp8, scale):
+    """Scores far below and far beyond the cap, turned round, and all zero."""
+    for qlens in (None, [40]):
+        b = R.build(64, [200], qlens, 8, 1, 128, 16, dtype, fp8)
+        b["scale"] = scale
+        cap = 0.01 if scale == 1e-6 else 30.0
+        # The tolerance's d_j = (D + 8) 2^-23 scale sum |q| |K| bounds an error's size only for scale >= 0 (below, it
+        # is minus the bound). scale q.K = |scale| (-q).K, and -q is exact: the definition over the negated queries is
+        # the same one, with d_j >= 0.
+        ref, tol = R.reference(b if scale >= 0 else dict(b, q=-b["q"], scale=-scale), softcap=cap)
+        assert R.worst(call(b, softcap=cap), ref, tol) <= 1.0
