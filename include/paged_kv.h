@@ -565,7 +565,7 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  * attention without a causal mask. Their values need not be sorted, and may
  * lie outside the context (they are clamped to it).
  *
- *   softcap        finite and >= 0; 0 is no cap
+ *   softcap        >= 0 and at most 1e30; 0 is no cap
  *   alibi_slopes   [num_heads] fp32 device memory, or NULL
  *   window         >= 0; 0 is no window. The token's own position counts
  *   key_begin      [num_query_tokens] int32 (decode: [num_seqs]) device memory, or NULL

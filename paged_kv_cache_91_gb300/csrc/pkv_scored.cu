@@ -140,8 +140,10 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if (c.block_size != 8 && c.block_size != 16 && c.block_size != 32)
     return fail(PKV_ERR_UNSUPPORTED, "block_size %d (supported: 8, 16, 32)", c.block_size);
   if (!isfinite(c.scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
-  if (!(isfinite(c.softcap) && c.softcap >= 0.f))
-    return fail(PKV_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
+  // (2 log2(e) softcap must not overflow, nor scale / softcap -- over an FP8 pool times a row's power of two -- lose
+  // the scores among subnormal numbers: a product of up to 2^15 * 448 * 128 times their step 2^-149 and softcap)
+  if (!(c.softcap >= 0.f && c.softcap <= 1e30f))
+    return fail(PKV_ERR_INVALID_ARG, "softcap must be in [0, 1e30] (0: no cap)");
   if (c.window < 0) return fail(PKV_ERR_INVALID_ARG, "window must be >= 0 (0: no window)");
   if (c.fp8 && !(isfinite(c.k_scale) && isfinite(c.v_scale) && c.k_scale > 0.f && c.v_scale > 0.f))
     return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");

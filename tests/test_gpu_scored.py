@@ -554,3 +554,11 @@ def test_scales_far_from_the_cap(dtype, fp8, scale):
         # the same one, with d_j >= 0.
         ref, tol = R.reference(b if scale >= 0 else dict(b, q=-b["q"], scale=-scale), softcap=cap)
         assert R.worst(call(b, softcap=cap), ref, tol) <= 1.0
+
+
+@pytest.mark.parametrize("dtype,fp8", [("bf16", True), ("f16", True), ("bf16", False)])
+def test_the_largest_cap_is_no_cap(dtype, fp8):
+    for qlens in (None, [40]):
+        b = R.build(65, [200], qlens, 8, 1, 128, 16, dtype, fp8)
+        ref, tol = R.reference(b)
+        assert R.worst(call(b, softcap=1e30), ref, tol) <= 1.0

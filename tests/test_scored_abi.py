@@ -219,3 +219,13 @@ def test_arrays_side_by_side_are_not_refused_as_overlapping(lib):
     for kw in (a, none):
         reserve(lib, **kw)  # (refused for want of a device here, if at all)
         assert b"overlap" not in lib.pkv_last_error_message()
+
+
+@pytest.mark.parametrize("call", [decode, multi_query])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_caps_whose_factors_leave_the_range_are_refused(lib, call, fp8):
+    """2 log2(e) softcap has to be finite in fp32 (2.88 * 1.18e38 is not), and scale / softcap far from subnormal."""
+    for cap in (1.1e30, 1e38, 3.4e38):
+        assert call(lib, fp8, softcap=cap) == INVALID
+        assert b"softcap" in lib.pkv_last_error_message()
+    assert call(lib, fp8, softcap=1e30, num_seqs=0) == OK
