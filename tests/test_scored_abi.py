@@ -229,3 +229,16 @@ def test_caps_whose_factors_leave_the_range_are_refused(lib, call, fp8):
         assert call(lib, fp8, softcap=cap) == INVALID
         assert b"softcap" in lib.pkv_last_error_message()
     assert call(lib, fp8, softcap=1e30, num_seqs=0) == OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_grid_of_empty_places_is_refused(lib, fp8):
+    """max_query_len times the sequences: 2^27 places for row tiles, and no more (2048 of them a sequence and kv head)."""
+    kw = dict(num_heads=32, num_kv_heads=8, max_query_len=131072, max_context_len=131072, max_blocks_per_seq=8192,
+              num_query_tokens=65535)
+    assert multi_query(lib, fp8, **kw, num_seqs=8193) == UNSUPPORTED
+    assert b"max_query_len" in lib.pkv_last_error_message()
+    assert multi_query(lib, fp8, **kw, num_seqs=8192, out=None) == INVALID  # (the next check)
+    assert multi_query(lib, fp8, **dict(kw, max_query_len=4), num_seqs=65535, out=None) == INVALID
+    assert multi_query(lib, fp8, **dict(kw, max_query_len=524280, max_context_len=1 << 30, max_blocks_per_seq=1 << 27,
+                                        num_query_tokens=1 << 20), num_seqs=65535) == UNSUPPORTED
