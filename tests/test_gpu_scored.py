@@ -562,3 +562,55 @@ def test_the_largest_cap_is_no_cap(dtype, fp8):
         b = R.build(65, [200], qlens, 8, 1, 128, 16, dtype, fp8)
         ref, tol = R.reference(b)
         assert R.worst(call(b, softcap=1e30), ref, tol) <= 1.0
+
+
+@pytest.mark.parametrize("dtype,fp8", [("f16", False), ("bf16", True), ("bf16", False)])
+@pytest.mark.parametrize("qlens", [None, [20]])
+def test_many_keys_below_the_smallest_16_bit_weight(dtype, fp8, qlens):
+    """One key, and 16383 that weigh 2^-26 or 2^-24 of it each: below f16's steps, and together 2^-11 of the row."""
+    n, H, D = 16384, 8, 128
+    b = R.build(66, [n], qlens, H, 1, D, 16, dtype, fp8, spread=0.0)
+    b["q"][:] = 0
+    b["q"][:, :, 0] = 16.0
+    b.update(scale=1.0, k_scale=0.0625 if fp8 else 1.0, v_scale=2.0 ** -6 if fp8 else 1.0)
+    ln2 = 0.6931471805599453
+    for name, low, top in (("kc", -25.0 * ln2 / 16, 0.0), ("vc", -1.0, 1.0)):
+        per = b["k_scale"] if name == "kc" else b["v_scale"]
+        kind = torch.float8_e4m3fn if fp8 else b["dtype"]
+        pool = torch.zeros(b[name].shape, dtype=torch.float64)
+        pool[..., 0] = low / per
+        if name == "vc":
+            pool[:] = low / per
+        first = b["tables"][0, 0]
+        pool[first, :, 3] = top / per
+        b[name] = pool.to(kind).view(torch.uint8) if fp8 else pool.to(kind)
+    check(b)
+
+
+LONG = [  # H, Hkv, dtype, fp8, contexts, query lengths: contexts above 8192, split by the call itself or not at all
+    (8, 2, "bf16", False, [16384, 9001], None), (8, 2, "f16", False, [16384, 9001], None),
+    (8, 1, "bf16", True, [16384, 9001], None), (24, 1, "f16", False, [12000], None),
+    (8, 1, "bf16", False, [16384, 70], [9, 40]), (8, 1, "f16", False, [16384, 70], [9, 40]),
+    (8, 1, "bf16", True, [16384, 70], [9, 40]), (8, 1, "f16", True, [10000, 9000], [40, 3]),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,dtype,fp8,ctx,qlens", LONG)
+def test_long_contexts(H, Hkv, dtype, fp8, ctx, qlens):
+    """Contexts of up to 16384 tokens, with the partitions that the call chooses."""
+    b = R.build(67, ctx, qlens, H, Hkv, 128, 16, dtype, fp8)
+    check(b, softcap=5.0)
+    check(b, slopes=R.slopes_of(H) / 64, window=8200)
+
+
+@pytest.mark.parametrize("B,dtype,fp8", [(8, "f16", False), (32, "bf16", True)])
+def test_a_long_prompt(B, dtype, fp8):
+    """700 tokens behind 8000 others under a document mask: many row tiles, each of many tiles of keys."""
+    b = R.build(68, [8700], [700], 4, 1, 128, B, dtype, fp8)
+    begin = [t * 11 % 8000 for t in range(700)]
+    rows = list(range(0, 700, 23)) + [699]
+    out = call(b, key_begin=begin, softcap=8.0)
+    for t in rows:  # (row by row: the definition of a token alone)
+        one = dict(b, ctx=[8000 + t + 1], qlens=[1], q=b["q"][t:t + 1], starts=[0, 1])
+        ref, tol = R.reference(one, key_begin=[begin[t]], softcap=8.0)
+        assert R.worst(out[t:t + 1], ref, tol) <= 1.0
