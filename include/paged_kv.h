@@ -592,8 +592,8 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  * paged_attention_multi_query (a bad query_start_loc skips its sequence and
  * sets PKV_DEVERR_QUERY; a bad block id skips its tokens and sets
  * PKV_DEVERR_BLOCK_ID). Rows of out past the last sequence are not written.
- * max_query_len at most 524280, max_context_len at most 2^30. With more than 16
- * rows (query tokens times heads) per kv head, num_seqs * num_kv_heads *
+ * max_query_len at most 524280, max_context_len at most 2^30. With more than 24
+ * rows (query tokens times heads) per kv head (E4M3: 40), num_seqs * num_kv_heads *
  * partitions * ceil(max_query_len * (num_heads / num_kv_heads) / 256) at most
  * 2^27: max_query_len should be near the longest query, since every sequence's
  * place in the grid is of that length.

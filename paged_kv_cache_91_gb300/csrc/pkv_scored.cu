@@ -48,9 +48,13 @@ struct ScoredPlan {
   size_t partials;  // bytes
 };
 
-// Rows per kv head from which the tensor-memory tile runs (one number for 16-bit and FP8 pools: the workspace
-// size does not know the pool's type).
-constexpr int kScoredTensorRows = 17;
+// Rows per kv head (query tokens times heads) from which the tensor-memory tile runs. Measured, us a call, 8-column
+// and tensor tile, 64 contexts of 1500 to 4096 tokens with a cap:
+//   decode, 2 kv heads    16-bit pool: 24 rows 61, 84; 32 rows 75, 89; 40 rows 89, 90; 48 rows 104, 91
+//                         E4M3: 24 rows 58, 98; 32 rows 75, 116; 40 rows 90, 118; 48 rows 104, 117; 64 rows 133, 119
+//   multi-query, 4 heads  16-bit pool: 16 rows 150, 209; 24 rows 202, 209; 32 rows 262, 232
+//   a kv head, 8 of them  E4M3: 24 rows 200, 279; 32 rows 259, 349; 48 rows 373, 351
+int tensor_rows(bool fp8, int max_query_len) { return fp8 ? 41 : max_query_len > 1 ? 25 : 33; }
 // Partition sizes as in paged_attention_decode. A small batch is split further: up to three CTAs an SM (tensor
 // tile: one), as long as a partition keeps 512 (384) tokens. Measured, us a call: one context of 16384 tokens, 32/8
 // heads, 2048-token partitions 29.0, 512 24.1, 256 25.9; 16 contexts of up to 4096, 32 heads on one kv head (tensor
@@ -67,12 +71,12 @@ long long scored_span_bound(int block_size, int max_query_len, int max_context_l
   return window > 0 && w < max_context_len ? w : max_context_len;
 }
 
-ScoredPlan scored_plan(int num_query_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+ScoredPlan scored_plan(bool fp8, int num_query_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
                        int max_query_len, int max_context_len, int window, int partition_size,
                        size_t workspace_bytes = SIZE_MAX) {
   ScoredPlan pl{};
   const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
-  pl.tensor = rows >= kScoredTensorRows;
+  pl.tensor = rows >= tensor_rows(fp8, max_query_len);
   pl.row_tiles = (int)(pl.tensor ? (rows + 255) / 256 : (rows + 7) / 8);
   const long long span = scored_span_bound(block_size, max_query_len, max_context_len, window);
   if (partition_size) {
@@ -174,7 +178,7 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
     return fail(PKV_ERR_UNSUPPORTED, "pool rows num_blocks * num_kv_heads * block_size must be < 2^31");
   if ((long long)c.num_query_tokens * c.num_heads >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "num_query_tokens * num_heads must be < 2^31");
-  const ScoredPlan pl = scored_plan(c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
+  const ScoredPlan pl = scored_plan(c.fp8, c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
                                     c.max_query_len, c.max_context_len, c.window, c.partition_size,
                                     c.workspace ? c.workspace_bytes : 0);
   if ((long long)pl.np * pl.row_tiles >= (1LL << 31))
@@ -289,9 +293,14 @@ size_t paged_attention_scored_workspace_size(int32_t num_query_tokens, int32_t n
   if (num_query_tokens <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
       block_size <= 0 || max_query_len <= 0 || max_context_len < 0 || window < 0 || partition_size < 0)
     return 0;
-  return scored_plan(num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len, max_context_len,
-                     window, partition_size)
-      .partials;
+  size_t bytes = 0;  // for either type of pool
+  for (bool fp8 : {false, true}) {
+    const size_t n = scored_plan(fp8, num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                                 max_context_len, window, partition_size)
+                         .partials;
+    if (n > bytes) bytes = n;
+  }
+  return bytes;
 }
 
 pkv_status_t paged_attention_decode_scored(void* out, const void* query, const void* key_cache,

@@ -642,3 +642,27 @@ def test_a_bad_value_that_all_rows_see_is_looked_for_once():
         medians.append(sorted(times)[4])
     assert torch.isnan(out).all()
     assert medians[1] < 20 * medians[0]
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", [
+    (32, 1, 128, 16, "f16", False), (33, 1, 128, 16, "bf16", False), (72, 2, 64, 8, "f16", False),
+    (40, 1, 128, 16, "bf16", True), (41, 1, 128, 16, "bf16", True), (96, 2, 128, 32, "f16", True),
+])
+def test_decode_with_many_heads_on_a_kv_head(H, Hkv, D, B, dtype, fp8, rule):
+    """On both sides of the rows from which the 256-row tile runs, and split over long contexts by the call."""
+    b = R.build(69, [2600, 300, 0, 1, 77], None, H, Hkv, D, B, dtype, fp8)
+    check(b, **rules_of(rule, b))
+
+
+@pytest.mark.parametrize("H,q", [(4, 6), (4, 7), (8, 3), (8, 4), (8, 5), (8, 6)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_workspace_serves_either_pool(H, q, fp8):
+    """The size that the query gives is enough whichever tile the pool's type takes."""
+    b = R.build(70, [2600, 1900], [q, q - 1], H, 1, 128, 16, "bf16", fp8)
+    need = binding.paged_attention_scored_workspace_size(2 * q - 1, H, 1, 128, 16, q, 2600)
+    ws = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+    ref, tol = R.reference(b, softcap=5.0)
+    out = call(b, softcap=5.0, workspace=ws[:need] if need else None)
+    assert R.worst(out, ref, tol) <= 1.0
+    assert (ws[need:] == 0x5A).all() and binding.device_errors() == 0
