@@ -57,8 +57,8 @@ struct ScoredPlan {
 int tensor_rows(bool fp8, int max_query_len) { return fp8 ? 41 : max_query_len > 1 ? 25 : 33; }
 // Partition sizes as in paged_attention_decode. A small batch is split further: up to three CTAs an SM (tensor
 // tile: one), as long as a partition keeps 512 (384) tokens. Measured, us a call: one context of 16384 tokens, 32/8
-// heads, 2048-token partitions 29.0, 512 24.1, 256 25.9; 16 contexts of up to 4096, 32 heads on one kv head (tensor
-// tile), unsplit 63.5, 1024 25.8, 384 23.9, 256 27.0, 128 35.9.
+// heads, 2048-token partitions 31.4, 1024 20.3, 512 19.1, 256 23.4; 16 contexts of 2000 to 4096, 48 heads on one kv
+// head (tensor tile), 2048-token partitions 36.7, 1024 24.9, 512 22.0, 384 23.9, 256 27.6, 128 39.0.
 constexpr int kScoredPartition = 1024, kScoredPartitionLong = 2048, kScoredLong = 8192;
 constexpr int kScoredFill = 456, kScoredFillTensor = 152, kScoredMin = 512, kScoredMinTensor = 384;
 

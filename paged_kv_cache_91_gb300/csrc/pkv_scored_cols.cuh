@@ -5,10 +5,11 @@
 //
 // A tile's products become scores in registers (ScoredRule): some 8 instructions a score beside the 2 * D * 2
 // bytes of K and V that up to 8 rows share, so over a 16-bit pool the kernel stays bound by reading them (256
-// contexts, 32/8 heads, cap 50, window 1024: 155 us, 6.7 TB/s; 12 contexts of 9001 to 16384 tokens, 40 heads,
-// distance biases: 451 us, 7.1 TB/s). An E4M3 pool halves the bytes, and the widening of its codes bounds it (128
-// contexts to 4096 tokens, 64/8 heads, cap 30: 120 us, 5.3 TB/s). Only the blocks between the CTA's first and last
-// visible key are copied.
+// contexts, 32/8 heads, cap 50, window 1024: 154 us, 6.6 TB/s; 12 contexts of 9001 to 16384 tokens, 40 heads,
+// distance biases: 462 us, 7.2 TB/s). An E4M3 pool halves the bytes and the widening of its codes doubles the
+// instructions a byte: no unit is full (issue slots 47 %, HBM 71 %), and warps wait for their copies most (128 contexts
+// to 4096 tokens, 64/8 heads, cap 30: 121 us, 5.3 TB/s). Only the blocks between the CTA's first and last visible key
+// are copied.
 #pragma once
 
 #include "pkv_scored.cuh"

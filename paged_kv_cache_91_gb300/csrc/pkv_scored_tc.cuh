@@ -14,9 +14,9 @@
 // second tile, and their (m, l, O) are merged at the end.
 //
 // What bounds it: per 256 x 128 scores the tensor cores need about 2048 cycles (head_dim 128), the shared memory
-// port 2500 (Q for every half, K and V for both streams, the copies once) and the exponentials 1024; measured are
-// 3500 without and 4300 with a cap (1170 and 980 TFLOP/s of visible scores, a causal prompt of 8192 tokens, 32/8
-// heads), with no unit saturated: it is the chain from S to P in the row threads. So a score is kept to few
+// port 2500 (Q for every half, K and V for both streams, the copies once) and the exponentials 1024; a CTA takes 4000
+// without and 4700 with a cap over its tiles (468 and 552 us, 1170 and 1000 TFLOP/s of visible scores, a causal prompt
+// of 8192 tokens, 32/8 heads), with no unit saturated: it is the chain from S to P in the row threads. So a score is kept to few
 // instructions: tiles that every row sees whole skip the masks, the tanh is a polynomial where the tile's scores
 // stay well below the cap, and both are computed on pairs.
 //
@@ -32,7 +32,8 @@
 // blocks of K and V tiles, half of each tile a warp (a copy takes about 100 cycles to issue), into a ring of
 // tile slots in the order K0 V0 K1 V1 ..., and 10 finds the items; FP8 pool: 12-15 widen a tile's codes to f16
 // in place. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set
-// PKV_DEVERR_TIMEOUT and write zeros for the item's rows.
+// PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has already claimed
+// for later stay as they were.
 #pragma once
 
 #include <type_traits>
