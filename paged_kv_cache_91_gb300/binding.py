@@ -126,13 +126,20 @@ def _stream(t: torch.Tensor, stream):
     return stream.cuda_stream
 
 
+def _torch_stream(stream, like: torch.Tensor):
+    """The call's stream (None: the current one) as torch's: another library's is known by its handle."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream) and hasattr(stream, "cuda_stream"):
+        return torch.cuda.ExternalStream(stream.cuda_stream, device=like.device)
+    return stream
+
+
 def _new_workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
     """A workspace for one call on `stream` (None: the current one), from the memory that the allocator keeps for that
     stream: memory freed on another one may still be in use by work queued there, and is given out again only in the
     order of its own stream."""
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, like)):
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 

@@ -81,3 +81,21 @@ def test_memory_freed_on_the_current_stream_is_not_taken(cuda_lib, monkeypatch):
     call(side)
     assert made[0].numel() == size and made[0].data_ptr() != at
     torch.cuda.synchronize()
+
+
+class Handle:
+    """A stream of another library: a handle and no more."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("name", ["decode", "multi_query", "shared_prefix", "decode_scored", "multi_query_scored"])
+def test_a_stream_known_by_its_handle(cuda_lib, name):
+    call = calls(False)[name]
+    want = call(None).clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = call(Handle(side))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
