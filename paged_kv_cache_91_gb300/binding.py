@@ -126,6 +126,13 @@ def _stream(t: torch.Tensor, stream):
     return stream.cuda_stream
 
 
+def _longest_query(query_start_loc: torch.Tensor, stream) -> int:
+    """The longest query, read (and waited for) behind the work that is queued on the call's stream: the offsets may be
+    made there."""
+    with torch.cuda.stream(_torch_stream(stream, query_start_loc)):
+        return int((query_start_loc[1:] - query_start_loc[:-1]).max().item())
+
+
 def _torch_stream(stream, like: torch.Tensor):
     """The call's stream (None: the current one) as torch's: another library's is known by its handle."""
     if stream is not None and not isinstance(stream, torch.cuda.Stream) and hasattr(stream, "cuda_stream"):
@@ -361,7 +368,7 @@ def _multi_query(out, query, key_cache, value_cache, block_tables, context_lens,
     if max_context_len is None:
         max_context_len = maxb * B
     if max_query_len is None:
-        max_query_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
+        max_query_len = _longest_query(query_start_loc, stream) if S else 0
     if workspace is None:
         need = int(lib.paged_attention_multi_query_workspace_size(T, H, Hkv, D, B, max_context_len,
                                                                   partition_size))
@@ -388,7 +395,7 @@ def paged_attention_multi_query(out: torch.Tensor, query: torch.Tensor, key_cach
     query_start_loc [S+1] int32): sequence s's q_len tokens are its last q_len context positions.
 
     ``max_query_len`` bounds every q_len on the host; when omitted it is read from
-    query_start_loc, which synchronises the stream.
+    query_start_loc, which synchronises the call's stream.
     """
     return _multi_query(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale,
                         max_query_len, max_context_len, partition_size, workspace, stream, False, 1.0, 1.0)
@@ -556,7 +563,7 @@ def _scored(out, query, key_cache, value_cache, block_tables, context_lens, quer
         if query_start_loc.shape != (S + 1,):
             raise PagedKVError(-1, "query_start_loc must be [S + 1]")
         if max_query_len is None:
-            max_query_len = int((query_start_loc[1:] - query_start_loc[:-1]).max().item()) if S else 0
+            max_query_len = _longest_query(query_start_loc, stream) if S else 0
     slopes = begin = end = ws = None
     if alibi_slopes is not None:
         _expect("alibi_slopes", alibi_slopes, torch.float32, dev)
@@ -641,7 +648,7 @@ def paged_attention_multi_query_scored(out: torch.Tensor, query: torch.Tensor, k
     [key_begin[t], key_end[t]) (int32 [T]; default: from 0, to its own position), cut by the window and the context.
 
     ``max_query_len`` bounds every query length on the host; when omitted it is read from query_start_loc, which
-    synchronises the stream.
+    synchronises the call's stream.
     """
     return _scored(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, scale, softcap,
                    alibi_slopes, window, key_begin, key_end, max_query_len, max_context_len, partition_size,

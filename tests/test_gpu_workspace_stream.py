@@ -99,3 +99,25 @@ def test_a_stream_known_by_its_handle(cuda_lib, name):
     out = call(Handle(side))
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("wrap", [lambda s: s, Handle])
+def test_the_longest_query_is_read_on_the_calls_stream(cuda_lib, scored, wrap):
+    """query_start_loc is still being made on the call's stream when max_query_len is read from it."""
+    b = R.build(71, [200, 90], [40, 1], 8, 2, 128, 16)
+    ref, tol = R.reference(b)
+    q, kc, vc, bt = (b[k].to(DEV) for k in ("q", "kc", "vc", "tables"))
+    out, ctx, made = torch.full_like(q, float("nan")), i32(b["ctx"]), i32(b["starts"])
+    starts = i32([0, 1, 2])
+    fn = binding.paged_attention_multi_query_scored if scored else binding.paged_attention_multi_query
+    side = torch.cuda.Stream()
+    binding.device_errors(clear=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+        starts.copy_(made)
+    fn(out, q, kc, vc, bt, ctx, starts, b["scale"], max_context_len=200, stream=wrap(side))
+    torch.cuda.synchronize()
+    assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
