@@ -715,6 +715,7 @@ pkv_status_t paged_kv_reserve_slots(int32_t* block_tables, int32_t max_blocks_pe
  * outside [0, num_blocks) is pushed as -1 and sets PKV_DEVERR_BLOCK_ID (a
  * reserve refuses to hand it out); blocks past free_capacity are not written
  * and set PKV_DEVERR_BLOCK_ID, num_free_out then being free_capacity.
+ * max_blocks_per_seq * ceil(num_seqs / 304) < 2^31.
  */
 pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
                                      const int32_t* context_lens, const int32_t* finished, int32_t* free_blocks,

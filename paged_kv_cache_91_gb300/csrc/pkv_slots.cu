@@ -200,7 +200,7 @@ constexpr int kReleaseSeqs = kSlotThreads;  // most sequences per CTA
 __global__ void __launch_bounds__(kSlotThreads) pkv_release_blocks_kernel(const ReleaseParams p) {
   pdl_begin();
   __shared__ TwoSums ws[kSlotThreads / 32];
-  __shared__ int32_t s_at[kReleaseSeqs + 1];  // where each of the CTA's sequences starts among the CTA's blocks
+  __shared__ int32_t s_at[kReleaseSeqs + 1];  // where each of the CTA's sequences starts among the CTA's blocks (< 2^31)
   const int tid = threadIdx.x;
   const int s0 = blockIdx.x * p.per_cta, n = min(p.per_cta, p.num_seqs - s0);
   const long long limit = (long long)p.max_blocks_per_seq * p.block_size;
@@ -372,6 +372,9 @@ pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_bl
                        {"num_free", num_free, sizeof(int32_t)}};
   const pkv_status_t apart = check_apart(written, read);
   if (apart != PKV_OK) return apart;
+  const int per_cta = num_seqs > 304 ? (num_seqs + 303) / 304 : 1;  // about two CTAs per SM (at most 216 sequences each)
+  if ((long long)per_cta * max_blocks_per_seq >= 1LL << 31)
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq times %d sequences must be < 2^31", per_cta);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -386,7 +389,7 @@ pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_bl
   p.err = device_error_word(dev);
   if (!p.err) return fail(PKV_ERR_CUDA, "device error word unavailable on device %d", dev);
   p.num_seqs = num_seqs;
-  p.per_cta = num_seqs > 304 ? (num_seqs + 303) / 304 : 1;  // about two CTAs per SM (at most 216 sequences each)
+  p.per_cta = per_cta;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.free_capacity = free_capacity;
   p.block_size = block_size;

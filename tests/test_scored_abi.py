@@ -242,3 +242,15 @@ def test_a_grid_of_empty_places_is_refused(lib, fp8):
     assert multi_query(lib, fp8, **dict(kw, max_query_len=4), num_seqs=65535, out=None) == INVALID
     assert multi_query(lib, fp8, **dict(kw, max_query_len=524280, max_context_len=1 << 30, max_blocks_per_seq=1 << 27,
                                         num_query_tokens=1 << 20), num_seqs=65535) == UNSUPPORTED
+
+
+def test_release_refuses_more_blocks_than_it_counts(lib):
+    """A CTA counts its sequences' blocks in 32 bits: tables of 2^31 entries for the sequences of one are refused."""
+    apart = ("context_lens", "finished", "free_blocks", "num_free", "context_lens_out", "num_free_out")
+    kw = dict({n: P((i + 1) << 24) for i, n in enumerate(apart)}, block_size=8, block_tables=P(1 << 44))
+    wide = (1 << 28) - 16
+    assert release(lib, num_seqs=304 * 8 + 1, max_blocks_per_seq=wide, **kw) == UNSUPPORTED
+    assert b"2^31" in lib.pkv_last_error_message()
+    assert release(lib, num_seqs=65535, max_blocks_per_seq=(1 << 31) // 216 + 1, **kw) == UNSUPPORTED
+    release(lib, num_seqs=304 * 7, max_blocks_per_seq=wide, **kw)  # (seven sequences: not for that)
+    assert b"2^31" not in lib.pkv_last_error_message()
