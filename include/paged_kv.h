@@ -59,7 +59,8 @@ typedef enum {
 /* Bits of the per-device error word (see paged_kv_device_errors). */
 #define PKV_DEVERR_BLOCK_ID 1u /* a block-table entry outside [0, num_blocks)            */
 #define PKV_DEVERR_CONTEXT 2u  /* a context length < 0 or above max_context_len or
-                                  max_blocks_per_seq * block_size (clamped)               */
+                                  max_blocks_per_seq * block_size (clamped); a position
+                                  outside the table of angles                             */
 #define PKV_DEVERR_SLOT 4u     /* a slot_mapping entry >= num_blocks * block_size        */
 #define PKV_DEVERR_TIMEOUT 8u  /* a wait for a bulk copy gave up after its time limit   */
 #define PKV_DEVERR_QUERY 16u   /* query_start_loc gives a sequence a negative number of
@@ -722,6 +723,211 @@ pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_bl
                                      int32_t free_capacity, const int32_t* num_free, int32_t* context_lens_out,
                                      int32_t* num_free_out, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
                                      cudaStream_t stream);
+
+/*
+ * A speculative step whose drafted tokens form a tree. The pages name
+ * speculative decoding ("Sparse Computation and Memory Management for Efficient
+ * LLM Inference", Speculative Decoding) without an interface; these calls serve
+ * it over the same pool, block tables and slots as the calls above.
+ *
+ * A sequence's q_len drafted tokens are the last q_len slots of its context, in
+ * an order in which a token's parent comes before it: node u of sequence s is
+ * query row query_start_loc[s] + u, and its key and value lie at place c + u,
+ * where c = context_lens[s] - q_len tokens are committed. Its position (the one
+ * that keys are rotated by) is c + its depth. A step, all of it on the GPU:
+ *   paged_kv_reserve_slots      slots, offsets and contexts of the drafted tokens
+ *   paged_kv_tree_layout        their mask and positions
+ *   per layer: paged_kv_write_rope, paged_attention_tree
+ *   (the caller decides which path of each tree is accepted)
+ *   paged_kv_compact_accepted   the accepted rows move up behind the committed ones
+ *   paged_kv_trim_blocks        blocks behind the new context return to the stack
+ */
+
+/*
+ * paged_kv_tree_layout -- masks and positions of drafted trees, from the parents.
+ *
+ *   tree_mask[t]: bit u % 32 of word u / 32 is set for node u = the token itself
+ *                 and for each of its ancestors; every other bit is 0
+ *   positions[t] = context_lens[s] - q_len + depth (a root's depth is 0)
+ *
+ *   parents          [num_query_tokens] int32: the parent's node in the same tree,
+ *                    or a negative number for a root (any number of roots)
+ *   query_start_loc  [num_seqs + 1], context_lens [num_seqs] int32, as in
+ *                    paged_attention_tree
+ *   tree_mask        [num_query_tokens][mask_words] int32, written
+ *   positions        [num_query_tokens] int32, written
+ *   max_query_len    host bound on every q_len, at most 1024 and 32 * mask_words
+ *
+ * What is written must not overlap anything else of the call. A parent that does
+ * not come before its token counts as none, and sets PKV_DEVERR_QUERY. A sequence
+ * with bad offsets (as in paged_attention_multi_query), or with more drafted
+ * tokens than context, is skipped (its rows are not written) and sets
+ * PKV_DEVERR_QUERY. Rows past the last sequence are not written. num_seqs <=
+ * 65535. One launch, asynchronous on `stream`.
+ */
+pkv_status_t paged_kv_tree_layout(const int32_t* parents, const int32_t* query_start_loc, const int32_t* context_lens,
+                                  int32_t num_seqs, int32_t num_query_tokens, int32_t max_query_len,
+                                  int32_t* tree_mask, int32_t mask_words, int32_t* positions, cudaStream_t stream);
+
+/*
+ * paged_kv_write_rope -- paged_kv_write of keys that are normed per head and
+ * rotated by their position on the way, and the same for the queries.
+ *
+ * For each row x (token t, head) of query and key, in fp32:
+ *     x = x / sqrt(mean(x^2) + eps) * weight          if the row's weight is given
+ *     (x_a, x_b) = (x_a c - x_b s, x_b c + x_a s)     for i < rotary_dim / 2
+ *         c = cos_sin[positions[t]][i], s = cos_sin[positions[t]][rotary_dim / 2 + i]
+ *         (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved
+ * Dims from rotary_dim on are not rotated. Queries are rounded once, to the
+ * query dtype, into query_out[t]; keys once, to the pool's type, into the pool at
+ * slot_mapping[t]; value rows are copied there (the _fp8 form: quantized), as in
+ * paged_kv_write(_fp8).
+ *
+ *   query_out        [num_tokens][num_heads][head_dim], contiguous; may be query
+ *                    itself if that is contiguous too
+ *   query, key, value  rows of [heads][head_dim], one every *_stride elements (so
+ *                    that they may be parts of one projection's output); strides
+ *                    multiples of 8 elements, at least heads * head_dim
+ *   slot_mapping     [num_tokens] int64; a negative slot stores nothing (the
+ *                    query row is written all the same)
+ *   positions        [num_tokens] int32, cos_sin [max_position][rotary_dim] fp32
+ *                    (16-byte aligned), or both NULL with rotary_dim 0: no rotation
+ *   rotary_dim       a multiple of 16 up to head_dim
+ *   q_weight, k_weight  [head_dim] fp32, 16-byte aligned, or NULL: not normed
+ *   eps              >= 0 and finite
+ *
+ * The query, key and value arrays must not overlap the pool; query_out must not
+ * overlap key, value or the pool. A slot at or past num_blocks * block_size
+ * stores nothing and sets PKV_DEVERR_SLOT. A token with a position outside [0,
+ * max_position) gets a query row of zeros and stores nothing; it sets
+ * PKV_DEVERR_CONTEXT unless its slot is negative. Other arguments, limits and
+ * errors as in paged_kv_write(_fp8); num_heads need not be a multiple of
+ * num_kv_heads.
+ */
+pkv_status_t paged_kv_write_rope(void* query_out, const void* query, const void* key, const void* value,
+                                 void* key_cache, void* value_cache, const int64_t* slot_mapping,
+                                 const int32_t* positions, const float* cos_sin, int32_t max_position,
+                                 int32_t rotary_dim, int32_t interleaved, const float* q_weight,
+                                 const float* k_weight, float eps, int32_t num_tokens, int64_t query_stride,
+                                 int64_t key_stride, int64_t value_stride, int32_t num_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t block_size, int32_t num_blocks, pkv_dtype_t dtype,
+                                 cudaStream_t stream);
+
+pkv_status_t paged_kv_write_rope_fp8(void* query_out, const void* query, const void* key, const void* value,
+                                     void* key_cache, void* value_cache, const int64_t* slot_mapping,
+                                     const int32_t* positions, const float* cos_sin, int32_t max_position,
+                                     int32_t rotary_dim, int32_t interleaved, const float* q_weight,
+                                     const float* k_weight, float eps, int32_t num_tokens, int64_t query_stride,
+                                     int64_t key_stride, int64_t value_stride, int32_t num_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                     pkv_dtype_t dtype, float k_scale, float v_scale, cudaStream_t stream);
+
+/*
+ * paged_attention_tree -- attention of drafted trees over the paged pool.
+ *
+ * Query token t, node u of sequence s (above), sees the committed tokens, and of
+ * the drafted ones those in its mask:
+ *     x_j = scale * dot(query[t][h][:], K_j)
+ *     x_j = softcap * tanh(x_j / softcap)                if softcap > 0
+ *     out[t][h][:] = sum_j softmax(x)_j * V_j
+ *     over key_begin[t] <= j < context_lens[s] with j < c or bit j - c of
+ *     tree_mask[t] set                        (c = context_lens[s] - q_len)
+ * The mask is taken as it is (a token sees its own key only if its bit is set),
+ * and need not be that of a tree. A chain's mask gives
+ * paged_attention_multi_query. A token that sees no key gives zeros.
+ *
+ *   tree_mask    [num_query_tokens][mask_words] int32 device memory; bits from
+ *                q_len on are ignored. 32 * mask_words >= max_query_len
+ *   softcap      >= 0 and at most 1e30; 0 is no cap
+ *   key_begin    [num_query_tokens] int32 device memory, or NULL: 0. A sliding
+ *                window longer than the tree is deep is max(0, position - window
+ *                + 1); 2^31 - 1 hides everything (a sequence that waits, see
+ *                paged_kv_reserve_slots)
+ *   workspace    paged_attention_tree_workspace_size(...) bytes, 16-byte aligned;
+ *                may be NULL when that size is 0
+ *   *_fp8        over an E4M3 pool; head_dim 128 only
+ *
+ * Everything else (the other arguments and limits, precision, the error word,
+ * rows that are not seen, blocks that no token of a sequence sees) is as in
+ * paged_attention_multi_query_scored(_fp8).
+ */
+size_t paged_attention_tree_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t block_size, int32_t max_query_len,
+                                           int32_t max_context_len, int32_t partition_size);
+
+pkv_status_t paged_attention_tree(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                  int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                                  const int32_t* tree_mask, int32_t mask_words, float scale, float softcap,
+                                  const int32_t* key_begin, int32_t block_size, int32_t num_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+                                  int32_t partition_size, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+pkv_status_t paged_attention_tree_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                      int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                                      const int32_t* tree_mask, int32_t mask_words, float scale, float softcap,
+                                      const int32_t* key_begin, int32_t block_size, int32_t num_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+                                      float k_scale, float v_scale, int32_t partition_size, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * paged_kv_compact_accepted -- move the keys and values of each tree's accepted
+ * path up behind the committed tokens, in every layer.
+ *
+ * For i = 0 .. num_accepted[s] - 1, in this order, every layer and kv head: the
+ * K and V rows at place c + i of the sequence receive those of place
+ * c + accepted[s][i] (c = context_lens[s] - q_len, through the block table), bit
+ * for bit. The new context is c + num_accepted[s]; rows behind it are stale.
+ *
+ *   key_cache, value_cache  [num_layers][num_blocks][num_kv_heads][block_size][head_dim],
+ *                   16-byte aligned: the layers' pools one after another
+ *                   (num_layers 1: the ordinary pool). All use one block table
+ *   accepted        [num_seqs][max_accepted] int32: the path's nodes, root first,
+ *                   increasing
+ *   num_accepted    [num_seqs] int32, 0 .. max_accepted
+ *   query_start_loc, context_lens, block_tables   as in paged_attention_tree
+ *   dtype           of the pool: PKV_F16, PKV_BF16 or PKV_FP8_E4M3
+ *
+ * A sequence whose path is not increasing, leaves [0, q_len) or is longer than
+ * max_accepted, or whose offsets or context are bad, is left as it is and sets
+ * PKV_DEVERR_QUERY (a context above max_blocks_per_seq * block_size:
+ * PKV_DEVERR_CONTEXT). A row with a block id outside the pool at either end is not
+ * moved and sets PKV_DEVERR_BLOCK_ID. The blocks of a table are its sequence's
+ * alone. head_dim 64 or 128, block_size 8, 16 or 32; num_seqs <= 65535. One
+ * launch, asynchronous on `stream`.
+ */
+pkv_status_t paged_kv_compact_accepted(void* key_cache, void* value_cache, int32_t num_layers,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                       const int32_t* accepted, int32_t max_accepted, const int32_t* num_accepted,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                       int32_t num_blocks, pkv_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * paged_kv_trim_blocks -- cut sequences back to their first keep_lens[s] tokens,
+ * the blocks behind them back on the free stack of paged_kv_reserve_slots:
+ * drafted tokens that were not accepted, or a rollout that is taken back.
+ *
+ * For every s in order, the table entries ceil(keep_lens[s] / B) ..
+ * ceil(context_lens[s] / B) - 1 are appended at free_blocks[num_free[0]] and on,
+ * and context_lens_out[s] = keep_lens[s]. num_free_out[0] = num_free[0] + blocks
+ * pushed. The tables keep their entries. (keep_lens[s] = 0 is
+ * paged_kv_release_blocks.)
+ *
+ * Shapes, overlap rule, limits and checks as in paged_kv_release_blocks, with
+ * keep_lens in the place of finished; a keep_lens entry outside [0,
+ * context_lens[s]] is clamped and sets PKV_DEVERR_CONTEXT.
+ */
+pkv_status_t paged_kv_trim_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, const int32_t* keep_lens, int32_t* free_blocks,
+                                  int32_t free_capacity, const int32_t* num_free, int32_t* context_lens_out,
+                                  int32_t* num_free_out, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
+                                  cudaStream_t stream);
 
 /* Static string naming a status code. */
 const char* pkv_status_string(pkv_status_t status);

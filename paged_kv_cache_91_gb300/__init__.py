@@ -20,11 +20,19 @@ from .binding import (  # noqa: F401
     paged_attention_multi_query_workspace_size,
     paged_attention_scored_workspace_size,
     paged_attention_shared_prefix_workspace_size,
+    paged_attention_tree,
+    paged_attention_tree_fp8,
+    paged_attention_tree_workspace_size,
     paged_attention_workspace_size,
     paged_attention_workspace_size_fp8,
+    paged_kv_compact_accepted,
     paged_kv_copy_blocks,
     paged_kv_release_blocks,
     paged_kv_reserve_slots,
+    paged_kv_tree_layout,
+    paged_kv_trim_blocks,
     paged_kv_write,
     paged_kv_write_fp8,
+    paged_kv_write_rope,
+    paged_kv_write_rope_fp8,
 )

@@ -97,6 +97,23 @@ def load():
     lib.paged_kv_reserve_slots.argtypes = [P, i32, P, P, P, i32, P, P, i32, P, P, P, P, i32, i32, i32, P]
     lib.paged_kv_release_blocks.restype = i32
     lib.paged_kv_release_blocks.argtypes = [P, i32, P, P, P, i32, P, P, P, i32, i32, i32, P]
+    lib.paged_kv_trim_blocks.restype = i32
+    lib.paged_kv_trim_blocks.argtypes = lib.paged_kv_release_blocks.argtypes
+    lib.paged_kv_tree_layout.restype = i32
+    lib.paged_kv_tree_layout.argtypes = [P, P, P, i32, i32, i32, P, i32, P, P]
+    lib.paged_kv_compact_accepted.restype = i32
+    lib.paged_kv_compact_accepted.argtypes = [P, P, i32, P, i32, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, P]
+    lib.paged_attention_tree_workspace_size.restype = sz
+    lib.paged_attention_tree_workspace_size.argtypes = [i32] * 8
+    rope = [P] * 9 + [i32, i32, i32, P, P, f32, i32, i64, i64, i64, i32, i32, i32, i32, i32, i32]
+    tree = scored + [P, i32, i32, i32, i32, P, i32, f32, f32, P] + shape
+    for fp8 in ("", "_fp8"):
+        scales = [f32, f32] if fp8 else []
+        for name, args in ((f"paged_kv_write_rope{fp8}", rope + scales + [P]),
+                           (f"paged_attention_tree{fp8}", tree + scales + work)):
+            fn = getattr(lib, name)
+            fn.restype = i32
+            fn.argtypes = args
     _lib = lib
     return lib
 
@@ -731,6 +748,280 @@ def paged_kv_release_blocks(block_tables: torch.Tensor, context_lens: torch.Tens
                                 context_lens_out, num_free_out)
     _run_on(dev, stream, lib.paged_kv_release_blocks,
             (block_tables.data_ptr(), maxb, context_lens.data_ptr(), finished.data_ptr(), free_blocks.data_ptr(),
+             free_blocks.numel(), num_free.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(), S,
+             block_size, num_blocks))
+
+
+def _qkv_rows(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, tokens: int, heads: int, dim: int) -> int:
+    """The elements between tokens of t [tokens][heads][dim], whose tokens' rows are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        if not t.is_cuda:
+            raise PagedKVError(-1, f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise PagedKVError(-1, f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+        raise PagedKVError(-1, f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (tokens, heads, dim):
+        raise PagedKVError(-1, f"{name} must be [{tokens}][{heads}][{dim}], got {list(t.shape)}")
+    per_token, per_head, one = t.stride()
+    if one != 1 or (per_head != dim and heads > 1):
+        raise PagedKVError(-1, f"{name}: each token's heads must be contiguous")
+    return per_token if tokens > 1 else heads * dim
+
+
+def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, cos_sin, q_weight,
+                k_weight, eps, interleaved, stream, fp8, scales):
+    lib = _lib or load()
+    dtype = query.dtype
+    dt = _DTYPE.get(dtype)
+    dev = query.get_device()
+    if dt is None or dev < 0:
+        _cuda16("query", query)
+        raise PagedKVError(-1, "query must be a CUDA tensor")
+    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
+        if fp8:
+            _cuda_fp8(n, t)
+        _expect(n, t, t.dtype if fp8 else dtype, dev)
+    pool, shape = key_cache.shape, query.shape
+    if len(pool) != 4 or len(shape) != 3 or value_cache.shape != pool:
+        raise PagedKVError(-1, "the caches must be [blocks][kv heads][block size][head dim], query [tokens][heads][head "
+                               "dim]")
+    NB, Hkv, B, D = pool
+    T, H, D2 = shape
+    if D2 != D:
+        raise PagedKVError(-1, f"head dim {D2} of query, {D} of the caches")
+    strides = (_qkv_rows("query", query, dtype, dev, T, H, D), _qkv_rows("key", key, dtype, dev, T, Hkv, D),
+               _qkv_rows("value", value, dtype, dev, T, Hkv, D))
+    _expect("query_out", query_out, dtype, dev)
+    if query_out.shape != shape:
+        raise PagedKVError(-1, "query_out must have query's shape")
+    _expect("slot_mapping", slot_mapping, torch.int64, dev)
+    if slot_mapping.shape != (T,):
+        raise PagedKVError(-1, "slot_mapping must have one entry per token")
+    at = angles = qw = kw = None
+    rotary = most = 0
+    if (positions is None) != (cos_sin is None):
+        raise PagedKVError(-1, "positions and cos_sin go together")
+    if cos_sin is not None:
+        _expect("positions", positions, torch.int32, dev)
+        _expect("cos_sin", cos_sin, torch.float32, dev)
+        if positions.shape != (T,) or cos_sin.dim() != 2:
+            raise PagedKVError(-1, "positions must have one entry per token, cos_sin be [max_position][rotary_dim]")
+        most, rotary = cos_sin.shape
+        at, angles = positions.data_ptr(), cos_sin.data_ptr()
+    if q_weight is not None:
+        _expect("q_weight", q_weight, torch.float32, dev)
+        if q_weight.shape != (D,):
+            raise PagedKVError(-1, "q_weight must have one entry per dim of a head")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _expect("k_weight", k_weight, torch.float32, dev)
+        if k_weight.shape != (D,):
+            raise PagedKVError(-1, "k_weight must have one entry per dim of a head")
+        kw = k_weight.data_ptr()
+    _run_on(dev, stream, lib.paged_kv_write_rope_fp8 if fp8 else lib.paged_kv_write_rope,
+            (query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
+             value_cache.data_ptr(), slot_mapping.data_ptr(), at, angles, most, rotary, 1 if interleaved else 0, qw, kw,
+             eps, T, *strides, H, Hkv, D, B, NB, dt, *scales))
+    return query_out
+
+
+def paged_kv_write_rope(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                        key_cache: torch.Tensor, value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                        positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                        q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None) -> torch.Tensor:
+    """paged_kv_write of keys normed per head (``k_weight`` [D] fp32; None: not normed) and rotated by ``positions``
+    [T] int32, and the same for the queries (into query_out, which may be query itself). ``cos_sin``
+    [max_position][rotary_dim] fp32 holds a position's cosines, then its sines; both None: no rotation. query, key and
+    value [T][heads][D] may be slices of one projection's output; pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1)
+    if ``interleaved``."""
+    return _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, cos_sin, q_weight,
+                       k_weight, eps, interleaved, stream, False, ())
+
+
+def paged_kv_write_rope_fp8(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                            key_cache: torch.Tensor, value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                            positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor], k_scale: float,
+                            v_scale: float, q_weight: Optional[torch.Tensor] = None,
+                            k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                            stream=None) -> torch.Tensor:
+    """paged_kv_write_rope into an E4M3 pool: code = E4M3(x / k_scale) of the rotated keys, likewise for values with
+    v_scale."""
+    return _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, cos_sin, q_weight,
+                       k_weight, eps, interleaved, stream, True, (k_scale, v_scale))
+
+
+def paged_kv_tree_layout(parents: torch.Tensor, query_start_loc: torch.Tensor, context_lens: torch.Tensor,
+                         tree_mask: torch.Tensor, positions: torch.Tensor, max_query_len: Optional[int] = None,
+                         stream=None) -> None:
+    """Masks and positions of drafted trees: from each token's parent ([T] int32, its node in the same tree, < 0: a
+    root) writes tree_mask [T][words] int32 (the bits of the token itself and its ancestors) and positions [T] int32
+    (committed tokens + depth). context_lens count the drafted tokens.
+
+    ``max_query_len`` bounds every tree on the host (at most 1024); when omitted it is read from query_start_loc, which
+    synchronises the call's stream.
+    """
+    lib = _lib or load()
+    _cuda_i32("parents", parents)
+    dev = parents.get_device()
+    i32 = torch.int32
+    for n, t in (("parents", parents), ("query_start_loc", query_start_loc), ("context_lens", context_lens),
+                 ("tree_mask", tree_mask), ("positions", positions)):
+        _expect(n, t, i32, dev)
+    T, S = parents.numel(), context_lens.numel()
+    if parents.shape != (T,) or context_lens.shape != (S,) or query_start_loc.shape != (S + 1,):
+        raise PagedKVError(-1, "parents must be [T], context_lens [S] and query_start_loc [S + 1]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T or positions.shape != (T,):
+        raise PagedKVError(-1, "tree_mask must be [T][words] and positions [T]")
+    if max_query_len is None:
+        max_query_len = _longest_query(query_start_loc, stream) if S else 0
+    _run_on(dev, stream, lib.paged_kv_tree_layout,
+            (parents.data_ptr(), query_start_loc.data_ptr(), context_lens.data_ptr(), S, T, max_query_len,
+             tree_mask.data_ptr(), tree_mask.shape[1], positions.data_ptr()))
+
+
+def paged_attention_tree_workspace_size(num_query_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                        block_size: int, max_query_len: int, max_context_len: int,
+                                        partition_size: int = 0) -> int:
+    return int(load().paged_attention_tree_workspace_size(num_query_tokens, num_heads, num_kv_heads, head_dim,
+                                                          block_size, max_query_len, max_context_len, partition_size))
+
+
+def _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, tree_mask, scale, softcap,
+          key_begin, max_query_len, max_context_len, partition_size, workspace, stream, fp8, scales):
+    lib = _lib or load()
+    dtype = query.dtype
+    dt = _DTYPE.get(dtype)
+    dev = query.get_device()
+    if dt is None or dev < 0 or not query.is_contiguous():
+        _cuda16("query", query)
+    _expect("out", out, dtype, dev)
+    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
+        if fp8:
+            _cuda_fp8(n, t)
+        _expect(n, t, t.dtype if fp8 else dtype, dev)
+    i32 = torch.int32
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start_loc", query_start_loc),
+                 ("tree_mask", tree_mask)):
+        _expect(n, t, i32, dev)
+    shape, pool, tables = query.shape, key_cache.shape, block_tables.shape
+    if len(pool) != 4 or len(shape) != 3 or len(tables) != 2:
+        raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim], query [rows][heads][head "
+                               "dim] and block_tables [S][max_blocks]")
+    NB, Hkv, B, D = pool
+    T, H, D2 = shape
+    S, maxb = tables
+    if D2 != D or out.shape != shape or value_cache.shape != pool:
+        raise PagedKVError(-1, "shape mismatch between query, out and caches")
+    if context_lens.shape != (S,) or query_start_loc.shape != (S + 1,):
+        raise PagedKVError(-1, "block_tables must be [S][max_blocks], context_lens [S] and query_start_loc [S + 1]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise PagedKVError(-1, "tree_mask must be [rows][words]")
+    words = tree_mask.shape[1]
+    if max_query_len is None:
+        max_query_len = _longest_query(query_start_loc, stream) if S else 0
+    if max_context_len is None:
+        max_context_len = maxb * B
+    begin = None
+    if key_begin is not None:
+        _expect("key_begin", key_begin, i32, dev)
+        if key_begin.shape != (T,):
+            raise PagedKVError(-1, "key_begin must have one entry per query row")
+        begin = key_begin.data_ptr()
+    ws, wbytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise PagedKVError(-1, "workspace must be a contiguous tensor on the query's device")
+        wbytes = workspace.numel() * workspace.element_size()
+    else:
+        wbytes = lib.paged_attention_tree_workspace_size(T, H, Hkv, D, B, max_query_len, max_context_len,
+                                                         partition_size)
+        if wbytes:
+            workspace = _new_workspace(wbytes, query, stream)
+    if workspace is not None:
+        ws = workspace.data_ptr()
+    _run_on(dev, stream, lib.paged_attention_tree_fp8 if fp8 else lib.paged_attention_tree,
+            (out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+             maxb, context_lens.data_ptr(), query_start_loc.data_ptr(), S, T, max_query_len, max_context_len,
+             tree_mask.data_ptr(), words, scale, softcap, begin, B, H, Hkv, D, NB, dt, *scales, partition_size, ws,
+             wbytes))
+    return out
+
+
+def paged_attention_tree(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                         tree_mask: torch.Tensor, scale: float, softcap: float = 0.0,
+                         key_begin: Optional[torch.Tensor] = None, max_query_len: Optional[int] = None,
+                         max_context_len: Optional[int] = None, partition_size: int = 0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of drafted trees (query/out [T][H][D], packed by query_start_loc [S + 1]): sequence s's q_len tokens
+    are its last q_len context positions, and each sees the committed positions before them and the drafted ones whose
+    bits are set in its tree_mask row ([T][words] int32, see paged_kv_tree_layout). ``softcap`` as in
+    paged_attention_decode_scored; ``key_begin`` [T] int32: a first visible key per token (a window, or 2**31 - 1 for
+    the tokens of a sequence that waits).
+
+    ``max_query_len`` bounds every tree on the host; when omitted it is read from query_start_loc, which synchronises
+    the call's stream.
+    """
+    return _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, tree_mask, scale,
+                 softcap, key_begin, max_query_len, max_context_len, partition_size, workspace, stream, False, ())
+
+
+def paged_attention_tree_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                             value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                             query_start_loc: torch.Tensor, tree_mask: torch.Tensor, scale: float, k_scale: float,
+                             v_scale: float, softcap: float = 0.0, key_begin: Optional[torch.Tensor] = None,
+                             max_query_len: Optional[int] = None, max_context_len: Optional[int] = None,
+                             partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """paged_attention_tree over an E4M3 pool (elements code * k_scale, code * v_scale); head_dim 128."""
+    return _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, tree_mask, scale,
+                 softcap, key_begin, max_query_len, max_context_len, partition_size, workspace, stream, True,
+                 (k_scale, v_scale))
+
+
+def paged_kv_compact_accepted(key_cache: torch.Tensor, value_cache: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, query_start_loc: torch.Tensor, accepted: torch.Tensor,
+                              num_accepted: torch.Tensor, stream=None) -> None:
+    """Move each tree's accepted path up behind the committed tokens: the K and V rows of node accepted[s][i] ([S][most]
+    int32, increasing) to the place of node i, for i < num_accepted[s] ([S] int32). The caches are one pool
+    [NB][Hkv][B][D], or the pools of all layers [layers][NB][Hkv][B][D]. context_lens count the drafted tokens."""
+    lib = _lib or load()
+    dev = key_cache.get_device()
+    dt = _cache_dtype("key_cache", key_cache)
+    _expect("value_cache", value_cache, key_cache.dtype, dev)
+    pool = key_cache.shape
+    if len(pool) not in (4, 5) or value_cache.shape != pool:
+        raise PagedKVError(-1, "the caches must both be [blocks][kv heads][block size][head dim], or that per layer")
+    i32 = torch.int32
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start_loc", query_start_loc),
+                 ("accepted", accepted), ("num_accepted", num_accepted)):
+        _expect(n, t, i32, dev)
+    layers = pool[0] if len(pool) == 5 else 1
+    NB, Hkv, B, D = pool[-4:]
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise PagedKVError(-1, "block_tables must be [S][max_blocks] and accepted [S][most]")
+    S, maxb = block_tables.shape
+    if context_lens.shape != (S,) or query_start_loc.shape != (S + 1,) or num_accepted.shape != (S,) or (
+            accepted.shape[0] != S):
+        raise PagedKVError(-1, "context_lens and num_accepted must be [S], query_start_loc [S + 1], accepted [S][most]")
+    _run_on(dev, stream, lib.paged_kv_compact_accepted,
+            (key_cache.data_ptr(), value_cache.data_ptr(), layers, block_tables.data_ptr(), maxb,
+             context_lens.data_ptr(), query_start_loc.data_ptr(), S, accepted.data_ptr(), accepted.shape[1],
+             num_accepted.data_ptr(), Hkv, D, B, NB, dt))
+
+
+def paged_kv_trim_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, keep_lens: torch.Tensor,
+                         free_blocks: torch.Tensor, num_free: torch.Tensor, context_lens_out: torch.Tensor,
+                         num_free_out: torch.Tensor, block_size: int, num_blocks: int, stream=None) -> None:
+    """Cut each sequence back to its first keep_lens[s] tokens ([S] int32): push the blocks behind them on the free
+    stack free_blocks (in place), and write context_lens_out [S] and num_free_out [1]. What is written must not overlap
+    anything else of the call."""
+    lib = _lib or load()
+    S, maxb, dev = _pool_arrays(block_tables, context_lens, "keep_lens", keep_lens, free_blocks, num_free,
+                                context_lens_out, num_free_out)
+    _run_on(dev, stream, lib.paged_kv_trim_blocks,
+            (block_tables.data_ptr(), maxb, context_lens.data_ptr(), keep_lens.data_ptr(), free_blocks.data_ptr(),
              free_blocks.numel(), num_free.data_ptr(), context_lens_out.data_ptr(), num_free_out.data_ptr(), S,
              block_size, num_blocks))
 

@@ -81,6 +81,15 @@ cudaError_t scored_tc_bf16(const DecodeParams& p, const ScoreParams& sc, const C
 cudaError_t scored_tc_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
 
+// Both over the drafted tokens of trees (ScoreParams::tree_mask).
+cudaError_t tree_cols(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                      bool f16, bool fp8, int head_dim, int block_size, int num_seqs, cudaStream_t stream);
+cudaError_t tree_tc_f16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        bool fp8, int head_dim, int block_size, int num_seqs, cudaStream_t stream);
+cudaError_t tree_tc_bf16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, bool fp8, int head_dim, int block_size, int num_seqs,
+                         cudaStream_t stream);
+
 // Tensor maps of the pool (cuTensorMapEncodeTiled); false if the driver refuses.
 bool make_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim, int block_size,
                    pkv_dtype_t dtype);

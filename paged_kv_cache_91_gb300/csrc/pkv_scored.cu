@@ -3,6 +3,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "paged_kv.h"
 #include "pkv_internal.h"
 #include "pkv_reduce.cuh"
@@ -14,7 +16,7 @@ namespace {
 // Merge of the partials of rows that span several partitions: a CTA takes 4 heads (a warp each) of
 // kReduceTokens query tokens of a sequence. Each row's first and last partition follow from its interval.
 constexpr int kReduceTokens = 8;
-template <typename T, int D>
+template <typename T, int D, bool TREE>
 __global__ void __launch_bounds__(32 * kReduceRows)
     pkv_scored_reduce_kernel(const DecodeParams p, const ScoreParams sc, int block_size) {
   pdl_begin();
@@ -27,7 +29,7 @@ __global__ void __launch_bounds__(32 * kReduceRows)
   const int base = scored_base(sc, ctx, q_len, block_size);
   for (int i = blockIdx.z * kReduceTokens; i < min(q_len, (int)(blockIdx.z + 1) * kReduceTokens); ++i) {
     int lo, hi;
-    scored_span(sc, q0 + i, ctx - q_len + i, ctx, lo, hi);
+    scored_span<TREE>(sc, q0 + i, ctx - q_len + i, ctx, lo, hi);
     const RowParts parts = row_parts(lo, hi, base, p.partition_size);
     if (parts.direct()) continue;  // written by the attention kernel
     const size_t row = (size_t)(q0 + i) * p.num_heads + h;
@@ -127,6 +129,9 @@ struct ScoredCall {
   void* workspace;
   size_t workspace_bytes;
   cudaStream_t stream;
+  bool tree = false;  // the query tokens are nodes of a tree; no distance bias, window or key_end then
+  const int32_t* tree_mask = nullptr;
+  int32_t mask_words = 0;
 };
 
 bool aligned(const void* ptr, uintptr_t n) { return (reinterpret_cast<uintptr_t>(ptr) & (n - 1)) == 0; }
@@ -165,6 +170,8 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if (!decode && c.max_query_len > c.max_context_len)
     return fail(PKV_ERR_INVALID_ARG, "max_query_len %d exceeds max_context_len %d", c.max_query_len,
                 c.max_context_len);
+  if (c.tree && (long long)c.mask_words * 32 < c.max_query_len)
+    return fail(PKV_ERR_INVALID_ARG, "mask_words %d: fewer bits than max_query_len %d", c.mask_words, c.max_query_len);
   if (c.partition_size < 0) return fail(PKV_ERR_INVALID_ARG, "partition_size < 0");
   if (c.partition_size && (c.partition_size % c.block_size || c.partition_size > kMaxPartitionBlocks * c.block_size))
     return fail(PKV_ERR_UNSUPPORTED, "partition_size %d must be a multiple of block_size in [%d, %d]",
@@ -191,7 +198,7 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
                 pl.row_tiles);
   if (c.num_seqs == 0 || c.num_query_tokens == 0 || c.max_query_len == 0) return PKV_OK;
   if (!c.out || !c.query || !c.key_cache || !c.value_cache || !c.block_tables || !c.context_lens ||
-      (!decode && !c.query_start_loc))
+      (!decode && !c.query_start_loc) || (c.tree && !c.tree_mask))
     return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(c.out, 16) || !aligned(c.query, 16) || !aligned(c.key_cache, 16) || !aligned(c.value_cache, 16))
     return fail(PKV_ERR_INVALID_ARG, "out, query and caches must be 16-byte aligned");
@@ -239,6 +246,8 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   sc.num_query_tokens = c.num_query_tokens;
   sc.max_query_len = c.max_query_len;
   sc.row_tiles = pl.row_tiles;
+  sc.tree_mask = reinterpret_cast<const uint32_t*>(c.tree_mask);
+  sc.mask_words = c.mask_words;
   if (c.softcap > 0.f) {
     sc.cap_in = scale / c.softcap;
     sc.cap_out = c.softcap * 1.4426950408889634f;
@@ -257,7 +266,11 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
                      !make_pool_map(&vmap, c.value_cache, pool_rows, c.head_dim, c.block_size, cache_dtype))
     return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
   const bool f16 = c.dtype == PKV_F16;
-  if (pl.tensor)
+  if (c.tree)
+    e = !pl.tensor ? tree_cols(p, sc, kmap, vmap, f16, c.fp8, c.head_dim, c.block_size, c.num_seqs, c.stream)
+        : f16      ? tree_tc_f16(p, sc, kmap, vmap, c.fp8, c.head_dim, c.block_size, c.num_seqs, c.stream)
+                   : tree_tc_bf16(p, sc, kmap, vmap, c.fp8, c.head_dim, c.block_size, c.num_seqs, c.stream);
+  else if (pl.tensor)
     e = c.fp8 ? scored_tc_fp8(p, sc, kmap, vmap, f16, c.block_size, c.num_seqs, c.stream)
         : f16 ? scored_tc_f16(p, sc, kmap, vmap, c.head_dim, c.block_size, c.num_seqs, c.stream)
               : scored_tc_bf16(p, sc, kmap, vmap, c.head_dim, c.block_size, c.num_seqs, c.stream);
@@ -271,10 +284,15 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
     auto reduce = [&](auto kern) {
       return launch_kernel(kern, grid, dim3(32 * kReduceRows), 0, c.stream, p, sc, (int)c.block_size);
     };
-    if (c.head_dim == 128)
-      e = f16 ? reduce(pkv_scored_reduce_kernel<__half, 128>) : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 128>);
-    else
-      e = f16 ? reduce(pkv_scored_reduce_kernel<__half, 64>) : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 64>);
+    auto of_tree = [&](auto tree) {
+      constexpr bool TREE = decltype(tree)::value;
+      if (c.head_dim == 128)
+        return f16 ? reduce(pkv_scored_reduce_kernel<__half, 128, TREE>)
+                   : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 128, TREE>);
+      return f16 ? reduce(pkv_scored_reduce_kernel<__half, 64, TREE>)
+                 : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 64, TREE>);
+    };
+    e = c.tree ? of_tree(std::true_type{}) : of_tree(std::false_type{});
     if (e != cudaSuccess) return cuda_fail(e, "scored reduce launch");
   }
   return PKV_OK;
@@ -360,6 +378,46 @@ pkv_status_t paged_attention_multi_query_scored_fp8(
                       query_start_loc, num_seqs, num_query_tokens, max_query_len, max_context_len, scale, softcap,
                       alibi_slopes, window, key_begin, key_end, block_size, num_heads, num_kv_heads, head_dim,
                       num_blocks, dtype, true, k_scale, v_scale, partition_size, workspace, workspace_bytes, stream},
+                     false);
+}
+
+size_t paged_attention_tree_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t block_size, int32_t max_query_len,
+                                           int32_t max_context_len, int32_t partition_size) {
+  return paged_attention_scored_workspace_size(num_query_tokens, num_heads, num_kv_heads, head_dim, block_size,
+                                               max_query_len, max_context_len, 0, partition_size);
+}
+
+pkv_status_t paged_attention_tree(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                  int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                                  const int32_t* tree_mask, int32_t mask_words, float scale, float softcap,
+                                  const int32_t* key_begin, int32_t block_size, int32_t num_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+                                  int32_t partition_size, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  return scored_impl({out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                      query_start_loc, num_seqs, num_query_tokens, max_query_len, max_context_len, scale, softcap,
+                      nullptr, 0, key_begin, nullptr, block_size, num_heads, num_kv_heads, head_dim, num_blocks, dtype,
+                      false, 1.f, 1.f, partition_size, workspace, workspace_bytes, stream, true, tree_mask, mask_words},
+                     false);
+}
+
+pkv_status_t paged_attention_tree_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                      int32_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                                      const int32_t* tree_mask, int32_t mask_words, float scale, float softcap,
+                                      const int32_t* key_begin, int32_t block_size, int32_t num_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, pkv_dtype_t dtype,
+                                      float k_scale, float v_scale, int32_t partition_size, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  return scored_impl({out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, context_lens,
+                      query_start_loc, num_seqs, num_query_tokens, max_query_len, max_context_len, scale, softcap,
+                      nullptr, 0, key_begin, nullptr, block_size, num_heads, num_kv_heads, head_dim, num_blocks, dtype,
+                      true, k_scale, v_scale, partition_size, workspace, workspace_bytes, stream, true, tree_mask,
+                      mask_words},
                      false);
 }
 

@@ -25,6 +25,8 @@ struct ScoreParams {
   float cap_in = 0.f;                   // scale / softcap
   float cap_out = 0.f;                  // softcap * log2(e); 0: no cap
   int row_tiles = 1;                    // row tiles per (partition, kv head, sequence)
+  const uint32_t* tree_mask = nullptr;  // [query tokens][mask_words], of the kernels for trees (TREE)
+  int mask_words = 0;
 };
 
 __device__ __forceinline__ float fast_rcp(float x) {
@@ -64,13 +66,32 @@ __device__ __forceinline__ int scored_query_len(const ScoreParams& sc, int s, in
   return q1 - q0;
 }
 
-// The visible keys [lo, hi) of query token t at position p in a context of ctx tokens (hi >= lo).
+// The visible keys [lo, hi) of query token t at position p in a context of ctx tokens (hi >= lo). TREE: the query
+// tokens are nodes of a tree, the context's last q_len positions; of those a token sees the ones in its mask, so that
+// its interval ends with the context.
+template <bool TREE = false>
 __device__ __forceinline__ void scored_span(const ScoreParams& sc, int t, int p, int ctx, int& lo, int& hi) {
+  if constexpr (TREE) {
+    lo = sc.key_begin ? max(0, sc.key_begin[t]) : 0;
+    hi = max(ctx, lo);
+    return;
+  }
   lo = sc.window > 0 && p >= sc.window ? p - sc.window + 1 : 0;
   if (sc.key_begin) lo = max(lo, sc.key_begin[t]);
   hi = p + 1;
   if (sc.key_end) hi = min(sc.key_end[t], ctx);
   hi = max(hi, lo);
+}
+
+// TREE: bit i says whether query token t sees the key of its sequence's node u + i; the keys before node 0 are
+// committed ones, which it does.
+__device__ __forceinline__ uint32_t tree_bits(const ScoreParams& sc, int t, int u) {
+  if (u <= -32) return 0xffffffffu;
+  const uint32_t* words = sc.tree_mask + (size_t)t * sc.mask_words;
+  const int w = u >> 5;  // (rounded down: -1 for u < 0)
+  const uint32_t a = w < 0 ? 0xffffffffu : w < sc.mask_words ? words[w] : 0u;
+  const uint32_t b = w + 1 < sc.mask_words ? words[w + 1] : 0u;
+  return __funnelshift_r(a, b, u & 31);
 }
 
 // A sequence's partitions: partition k holds the positions [base + k P, base + (k + 1) P), where base is the
@@ -112,8 +133,9 @@ __device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned cha
 // One row over the keys [a, b) on one warp: (m, l) and the output normalised by l. Lane t scores key t of 32, then
 // the lanes hold D / 32 dims each for their weighted values. The tiles multiply every key of a tile with every row,
 // a masked one with weight 0, and 0 times a NaN or infinite value is NaN: a row that such a value may have reached
-// is computed again here, where a masked key is not touched.
-template <typename T, typename C, int D>
+// is computed again here, where a masked key is not touched. pos: the row's position; TREE: that of node 0 (there is
+// no distance bias).
+template <typename T, typename C, int D, bool TREE = false>
 __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams& sc, size_t row, int s, int h,
                                         int pos, int a, int b, int block_size, int lane, float& m, float& l,
                                         float (&o)[D / 32]) {
@@ -128,7 +150,10 @@ __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams
   for (int j0 = a; j0 < b; j0 += 32) {
     const int j = j0 + lane;
     const int phys = j < b ? p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size] : -1;
-    const bool ok = (unsigned)phys < (unsigned)p.num_blocks;  // (a bad id is reported by the tile)
+    bool ok = (unsigned)phys < (unsigned)p.num_blocks;  // (a bad id is reported by the tile)
+    if constexpr (TREE) {
+      if (ok && j >= pos) ok = tree_bits(sc, (int)(row / p.num_heads), j - pos) & 1u;
+    }
     const size_t at = ok ? (((size_t)phys * p.num_kv_heads + g) * block_size + j % block_size) * D * EB : 0;
     float d = 0.f;
     if (ok) {

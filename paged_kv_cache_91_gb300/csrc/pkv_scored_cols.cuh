@@ -17,6 +17,7 @@
 
 namespace pkv {
 
+template <bool TREE>
 struct ScoredRule {
   float mul0, mul1;      // of the raw product: scale * log2(e), or scale / softcap
   float cap_out;         // softcap * log2(e), 0: no cap
@@ -26,6 +27,7 @@ struct ScoredRule {
   int pos0, pos1;        // the columns' positions
   int tok_base;          // position of the tile's token 0
   bool whole;            // every column of the warp sees every token of the tile
+  uint32_t see0, see1;   // TREE: bit t: the column sees token t of the tile, as far as the mask of its tree says
   __device__ __forceinline__ void operator()(float (&x)[4], int ta, bool va, int tb, bool vb) const {
     const int ja = tok_base + ta, jb = tok_base + tb;
     bool see[4] = {true, true, true, true};
@@ -34,6 +36,12 @@ struct ScoredRule {
       see[1] = va && (unsigned)(ja - lo1) < (unsigned)n1;
       see[2] = vb && (unsigned)(jb - lo0) < (unsigned)n0;
       see[3] = vb && (unsigned)(jb - lo1) < (unsigned)n1;
+      if constexpr (TREE) {
+        see[0] = see[0] && ((see0 >> ta) & 1u);
+        see[1] = see[1] && ((see1 >> ta) & 1u);
+        see[2] = see[2] && ((see0 >> tb) & 1u);  // (tb <= 31)
+        see[3] = see[3] && ((see1 >> tb) & 1u);
+      }
     }
     x[0] *= mul0;
     x[1] *= mul1;
@@ -77,7 +85,7 @@ struct ScoredRule {
 };
 
 // C: the cache's element type (the tile's T, or E4M3).
-template <typename Tile, typename C, int NW, int SPW>
+template <typename Tile, typename C, int NW, int SPW, bool TREE>
 __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
     pkv_scored_cols_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ ScoreParams sc,
                            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
   const int rn = row0 + min(lane >> 2, ncol - 1);
   const int tn = q0 + rn / G, hn = kvh * G + rn % G, pn = ctx - q_len + rn / G;
   int lo, hi;
-  scored_span(sc, tn, pn, ctx, lo, hi);
+  scored_span<TREE>(sc, tn, pn, ctx, lo, hi);
   const RowParts parts = row_parts(lo, hi, base, P);
   // the CTA's keys: from its rows' first to their last visible one, within the partition
   int c0 = hi > lo ? lo : INT32_MAX, c1 = hi > lo ? hi : 0;
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
   else
     Tile::load_qb_row(qb, qrow, lane);
   const int j0 = (lane & 3) * 2;  // its two accumulator columns
-  ScoredRule rule;
+  ScoredRule<TREE> rule;
   {
     const float mul = sc.cap_out != 0.f ? sc.cap_in : p.scale_log2;
     const float slope = sc.slopes ? sc.slopes[hn] * 1.4426950408889634f : 0.f;
@@ -213,6 +221,11 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
   for (int i = 0; i < nmine; ++i) {
     const int phys = __shfl_sync(kFull, my_phys, i);
     const int k = i % SPW;
+    uint32_t mine = 0;  // (read before the wait for the tile)
+    const int node0 = (blk0 + warp + NW * i) * BS - (ctx - q_len);  // node of the tile's token 0
+    if constexpr (TREE) {
+      if (node0 + BS > 0) mine = tree_bits(sc, tn, node0);
+    }
     const bool ready = __all_sync(kFull, mbar_wait(bars + k, (i / SPW) & 1));
     if (!ready) {
       failed_at = i;
@@ -225,6 +238,15 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
       // (a tile of 8 tokens fills half of the MMA's rows: its other rows are masked)
       rule.whole = BS >= 16 && first == 0 && nvalid == BS &&
                    __all_sync(kFull, lo <= rule.tok_base && rule.tok_base + BS <= hi);
+      if constexpr (TREE) {
+        if (node0 + BS > 0) {
+          rule.whole = false;
+          rule.see0 = __shfl_sync(kFull, mine, 4 * j0);
+          rule.see1 = __shfl_sync(kFull, mine, 4 * j0 + 4);
+        } else {
+          rule.see0 = rule.see1 = 0xffffffffu;
+        }
+      }
       Tile::fold(Ks, Ks + Sh::TILE, first, nvalid, qb, lane, m0, m1, l0, l1, acc, rule);
       if (first > 0 || nvalid < BS) zeroed |= 1u << k;
     }
@@ -290,19 +312,20 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
     const size_t row = (size_t)(q0 + r / G) * p.num_heads + h;
     // a non-finite row is a masked key's doing only if it misses some of the keys that the CTA multiplies, and not if
     // its own scores are NaN
-    if (!__all_sync(kFull, fine) && L == L && (nlo > c0 || nhi < c1))
-      scored_row<T, C, D>(p, sc, row, s, h, ctx - q_len + r / G, max(nlo, tok0), min(nhi, tok0 + P), BS, lane, M, L, o);
+    const int pos = ctx - q_len + (TREE ? 0 : r / G);
+    if (!__all_sync(kFull, fine) && L == L && (nlo > c0 || nhi < c1 || (TREE && c1 > pos)))
+      scored_row<T, C, D, TREE>(p, sc, row, s, h, pos, max(nlo, tok0), min(nhi, tok0 + P), BS, lane, M, L, o);
     store_row<T, D>(p, row, part, np.direct(), lane, M, L, o);
   }
 }
 
-template <typename Tile, typename C, int RING_BYTES = PKV_MMA_RING_BYTES>
+template <typename Tile, typename C, int RING_BYTES = PKV_MMA_RING_BYTES, bool TREE = false>
 cudaError_t launch_scored_cols(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int num_seqs, cudaStream_t stream) {
   constexpr int NW = kDecodeWarps;
   constexpr int SPW = mma_stages<2 * Tile::TILE, RING_BYTES>();
   using Sh = MmaShape<Tile::D, Tile::BS, NW, SPW, Tile::TILE>;
-  auto kern = pkv_scored_cols_kernel<Tile, C, NW, SPW>;
+  auto kern = pkv_scored_cols_kernel<Tile, C, NW, SPW, TREE>;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

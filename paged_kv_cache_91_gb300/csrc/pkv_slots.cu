@@ -1,9 +1,9 @@
 // Block tables and slot maps on the GPU: paged_kv_reserve_slots gives the next step's tokens their slots and
-// takes the new blocks from a free stack, paged_kv_release_blocks puts finished sequences' blocks back. Both
-// are one launch each, so that a step (reserve, cache write, attention, release) needs no host round trip and
-// can be captured in a graph.
+// takes the new blocks from a free stack, paged_kv_release_blocks puts finished sequences' blocks back and
+// paged_kv_trim_blocks those behind what a sequence keeps. Each is one launch, so that a step (reserve, cache write,
+// attention, release) needs no host round trip and can be captured in a graph.
 //
-// Both are prefix sums over the sequences followed by independent writes. A CTA does not wait for another
+// All are prefix sums over the sequences followed by independent writes. A CTA does not wait for another
 // one: each computes the sums that its own part needs from the request lengths, which stay in L2 (8 bytes per
 // sequence), instead of a second launch or a look-back. Bound by launch and memory latency.
 #include <stdint.h>
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kSlotThreads) pkv_reserve_slots_kernel(const R
 struct ReleaseParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
-  const int32_t* finished;
+  const int32_t* finished;  // (TRIM: keep_lens)
   int32_t* free_blocks;
   const int32_t* num_free;
   int32_t* context_lens_out;
@@ -196,19 +196,25 @@ struct ReleaseParams {
 constexpr int kReleaseSeqs = kSlotThreads;  // most sequences per CTA
 
 // CTA c pushes the blocks of the finished ones among sequences [c * per_cta, (c + 1) * per_cta), in order; it
-// sums the block counts of the sequences before its own itself.
+// sums the block counts of the sequences before its own itself. TRIM: a sequence's blocks behind the ones that it keeps.
+template <bool TRIM>
 __global__ void __launch_bounds__(kSlotThreads) pkv_release_blocks_kernel(const ReleaseParams p) {
   pdl_begin();
   __shared__ TwoSums ws[kSlotThreads / 32];
   __shared__ int32_t s_at[kReleaseSeqs + 1];  // where each of the CTA's sequences starts among the CTA's blocks (< 2^31)
+  __shared__ int32_t s_held[TRIM ? kReleaseSeqs : 1];  // TRIM: blocks that it keeps
   const int tid = threadIdx.x;
   const int s0 = blockIdx.x * p.per_cta, n = min(p.per_cta, p.num_seqs - s0);
   const long long limit = (long long)p.max_blocks_per_seq * p.block_size;
+  auto ceil_blocks = [&](long long n) { return (int)((n + p.block_size - 1) / p.block_size); };
+  auto context = [&](int s) -> long long {
+    const long long c = p.context_lens[s];
+    return c < 0 ? 0 : (c > limit ? limit : c);
+  };
+  auto kept = [&](int s) -> long long { return max(0ll, min((long long)p.finished[s], context(s))); };  // TRIM
   auto blocks = [&](int s) -> int {
-    if (!p.finished[s]) return 0;
-    long long c = p.context_lens[s];
-    c = c < 0 ? 0 : (c > limit ? limit : c);
-    return (int)((c + p.block_size - 1) / p.block_size);
+    if constexpr (TRIM) return ceil_blocks(context(s)) - ceil_blocks(kept(s));
+    return p.finished[s] ? ceil_blocks(context(s)) : 0;
   };
   int nfree = p.num_free[0];
   if (nfree < 0 || nfree > p.free_capacity) {
@@ -220,9 +226,16 @@ __global__ void __launch_bounds__(kSlotThreads) pkv_release_blocks_kernel(const 
   for (int s = tid; s < s0; s += kSlotThreads) v.a += blocks(s);
   if (tid < n) {
     const int c = p.context_lens[s0 + tid];
-    const bool gone = p.finished[s0 + tid] != 0;
-    if (gone && (c < 0 || c > limit)) atomicOr(p.err, PKV_DEVERR_CONTEXT);
-    p.context_lens_out[s0 + tid] = gone ? 0 : c;
+    if constexpr (TRIM) {
+      const int keep = (int)kept(s0 + tid);
+      if (c < 0 || c > limit || keep != p.finished[s0 + tid]) atomicOr(p.err, PKV_DEVERR_CONTEXT);
+      p.context_lens_out[s0 + tid] = keep;
+      s_held[tid] = ceil_blocks(keep);
+    } else {
+      const bool gone = p.finished[s0 + tid] != 0;
+      if (gone && (c < 0 || c > limit)) atomicOr(p.err, PKV_DEVERR_CONTEXT);
+      p.context_lens_out[s0 + tid] = gone ? 0 : c;
+    }
     v.b = blocks(s0 + tid);
   }
   const TwoSums at = block_exclusive(v, ws, total);
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(kSlotThreads) pkv_release_blocks_kernel(const 
       const int mid = (lo + hi) >> 1;
       if (s_at[mid] <= e) lo = mid; else hi = mid;
     }
-    int id = p.block_tables[(size_t)(s0 + lo) * p.max_blocks_per_seq + (e - s_at[lo])];
+    int id = p.block_tables[(size_t)(s0 + lo) * p.max_blocks_per_seq + (TRIM ? s_held[lo] : 0) + (e - s_at[lo])];
     const long long to = nfree + total.a + e;
     if ((unsigned)id >= (unsigned)p.num_blocks) {
       atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
@@ -286,6 +299,56 @@ pkv_status_t check_common(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t 
   if (num_seqs > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_seqs must be <= 65535");
   if ((long long)max_blocks_per_seq * block_size >= (1LL << 31) - 64)
     return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size must be < 2^31 - 64");
+  return PKV_OK;
+}
+
+// paged_kv_release_blocks (what: finished) and paged_kv_trim_blocks (what: keep_lens).
+template <bool TRIM>
+pkv_status_t release_impl(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                          const int32_t* what, int32_t* free_blocks, int32_t free_capacity, const int32_t* num_free,
+                          int32_t* context_lens_out, int32_t* num_free_out, int32_t num_seqs, int32_t block_size,
+                          int32_t num_blocks, cudaStream_t stream) {
+  set_last_error_message("");
+  const pkv_status_t st = check_common(num_seqs, max_blocks_per_seq, free_capacity, block_size, num_blocks);
+  if (st != PKV_OK) return st;
+  if (!num_free || !num_free_out || (free_capacity > 0 && !free_blocks) ||
+      (num_seqs > 0 && (!block_tables || !context_lens || !what || !context_lens_out)))
+    return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+  const size_t n = (size_t)num_seqs * sizeof(int32_t);
+  const Span written[] = {{"free_blocks", free_blocks, (size_t)free_capacity * sizeof(int32_t)},
+                          {"context_lens_out", context_lens_out, n},
+                          {"num_free_out", num_free_out, sizeof(int32_t)}};
+  const Span read[] = {{"block_tables", block_tables, n * (size_t)max_blocks_per_seq},
+                       {"context_lens", context_lens, n},
+                       {TRIM ? "keep_lens" : "finished", what, n},
+                       {"num_free", num_free, sizeof(int32_t)}};
+  const pkv_status_t apart = check_apart(written, read);
+  if (apart != PKV_OK) return apart;
+  const int per_cta = num_seqs > 304 ? (num_seqs + 303) / 304 : 1;  // about two CTAs per SM (at most 216 sequences each)
+  if ((long long)per_cta * max_blocks_per_seq >= 1LL << 31)
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq times %d sequences must be < 2^31", per_cta);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  ReleaseParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.finished = what;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.context_lens_out = context_lens_out;
+  p.num_free_out = num_free_out;
+  p.err = device_error_word(dev);
+  if (!p.err) return fail(PKV_ERR_CUDA, "device error word unavailable on device %d", dev);
+  p.num_seqs = num_seqs;
+  p.per_cta = per_cta;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.free_capacity = free_capacity;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  const unsigned grid = num_seqs > 0 ? (unsigned)((num_seqs + p.per_cta - 1) / p.per_cta) : 1u;
+  e = launch_kernel(pkv_release_blocks_kernel<TRIM>, dim3(grid), dim3(kSlotThreads), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, TRIM ? "paged_kv_trim_blocks launch" : "paged_kv_release_blocks launch");
   return PKV_OK;
 }
 
@@ -356,48 +419,17 @@ pkv_status_t paged_kv_release_blocks(const int32_t* block_tables, int32_t max_bl
                                      int32_t free_capacity, const int32_t* num_free, int32_t* context_lens_out,
                                      int32_t* num_free_out, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
                                      cudaStream_t stream) {
-  set_last_error_message("");
-  const pkv_status_t st = check_common(num_seqs, max_blocks_per_seq, free_capacity, block_size, num_blocks);
-  if (st != PKV_OK) return st;
-  if (!num_free || !num_free_out || (free_capacity > 0 && !free_blocks) ||
-      (num_seqs > 0 && (!block_tables || !context_lens || !finished || !context_lens_out)))
-    return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
-  const size_t n = (size_t)num_seqs * sizeof(int32_t);
-  const Span written[] = {{"free_blocks", free_blocks, (size_t)free_capacity * sizeof(int32_t)},
-                          {"context_lens_out", context_lens_out, n},
-                          {"num_free_out", num_free_out, sizeof(int32_t)}};
-  const Span read[] = {{"block_tables", block_tables, n * (size_t)max_blocks_per_seq},
-                       {"context_lens", context_lens, n},
-                       {"finished", finished, n},
-                       {"num_free", num_free, sizeof(int32_t)}};
-  const pkv_status_t apart = check_apart(written, read);
-  if (apart != PKV_OK) return apart;
-  const int per_cta = num_seqs > 304 ? (num_seqs + 303) / 304 : 1;  // about two CTAs per SM (at most 216 sequences each)
-  if ((long long)per_cta * max_blocks_per_seq >= 1LL << 31)
-    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq times %d sequences must be < 2^31", per_cta);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  ReleaseParams p{};
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.finished = finished;
-  p.free_blocks = free_blocks;
-  p.num_free = num_free;
-  p.context_lens_out = context_lens_out;
-  p.num_free_out = num_free_out;
-  p.err = device_error_word(dev);
-  if (!p.err) return fail(PKV_ERR_CUDA, "device error word unavailable on device %d", dev);
-  p.num_seqs = num_seqs;
-  p.per_cta = per_cta;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.free_capacity = free_capacity;
-  p.block_size = block_size;
-  p.num_blocks = num_blocks;
-  const unsigned grid = num_seqs > 0 ? (unsigned)((num_seqs + p.per_cta - 1) / p.per_cta) : 1u;
-  e = launch_kernel(pkv_release_blocks_kernel, dim3(grid), dim3(kSlotThreads), 0, stream, p);
-  if (e != cudaSuccess) return cuda_fail(e, "paged_kv_release_blocks launch");
-  return PKV_OK;
+  return release_impl<false>(block_tables, max_blocks_per_seq, context_lens, finished, free_blocks, free_capacity,
+                             num_free, context_lens_out, num_free_out, num_seqs, block_size, num_blocks, stream);
+}
+
+pkv_status_t paged_kv_trim_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, const int32_t* keep_lens, int32_t* free_blocks,
+                                  int32_t free_capacity, const int32_t* num_free, int32_t* context_lens_out,
+                                  int32_t* num_free_out, int32_t num_seqs, int32_t block_size, int32_t num_blocks,
+                                  cudaStream_t stream) {
+  return release_impl<true>(block_tables, max_blocks_per_seq, context_lens, keep_lens, free_blocks, free_capacity,
+                            num_free, context_lens_out, num_free_out, num_seqs, block_size, num_blocks, stream);
 }
 
 }  // extern "C"
