@@ -849,7 +849,9 @@ pkv_status_t paged_kv_write_rope_fp8(void* query_out, const void* query, const v
  *
  * Everything else (the other arguments and limits, precision, the error word,
  * rows that are not seen, blocks that no token of a sequence sees) is as in
- * paged_attention_multi_query_scored(_fp8).
+ * paged_attention_multi_query_scored(_fp8), but for the last limit: with more
+ * than 8 rows per kv head, num_seqs * num_kv_heads * partitions *
+ * ceil(max_query_len * (num_heads / num_kv_heads) / 128) at most 2^27.
  */
 size_t paged_attention_tree_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
                                            int32_t head_dim, int32_t block_size, int32_t max_query_len,

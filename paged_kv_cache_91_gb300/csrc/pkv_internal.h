@@ -81,7 +81,8 @@ cudaError_t scored_tc_bf16(const DecodeParams& p, const ScoreParams& sc, const C
 cudaError_t scored_tc_fp8(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                           const CUtensorMap& vmap, bool f16, int block_size, int num_seqs, cudaStream_t stream);
 
-// Both over the drafted tokens of trees (ScoreParams::tree_mask).
+// Tree attention (ScoreParams::tree_mask): the 8-column tile and the tensor-memory tile of 128 rows (pkv_tree_tc.cuh);
+// the pool as above.
 cudaError_t tree_cols(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap, const CUtensorMap& vmap,
                       bool f16, bool fp8, int head_dim, int block_size, int num_seqs, cudaStream_t stream);
 cudaError_t tree_tc_f16(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap, const CUtensorMap& vmap,

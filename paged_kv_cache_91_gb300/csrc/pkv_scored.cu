@@ -3,8 +3,6 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <type_traits>
-
 #include "paged_kv.h"
 #include "pkv_internal.h"
 #include "pkv_reduce.cuh"
@@ -16,7 +14,8 @@ namespace {
 // Merge of the partials of rows that span several partitions: a CTA takes 4 heads (a warp each) of
 // kReduceTokens query tokens of a sequence. Each row's first and last partition follow from its interval.
 constexpr int kReduceTokens = 8;
-template <typename T, int D, bool TREE>
+constexpr int kTreeReduceCtas = 4864;  // two waves of CTAs of four warps
+template <typename T, int D>
 __global__ void __launch_bounds__(32 * kReduceRows)
     pkv_scored_reduce_kernel(const DecodeParams p, const ScoreParams sc, int block_size) {
   pdl_begin();
@@ -29,7 +28,7 @@ __global__ void __launch_bounds__(32 * kReduceRows)
   const int base = scored_base(sc, ctx, q_len, block_size);
   for (int i = blockIdx.z * kReduceTokens; i < min(q_len, (int)(blockIdx.z + 1) * kReduceTokens); ++i) {
     int lo, hi;
-    scored_span<TREE>(sc, q0 + i, ctx - q_len + i, ctx, lo, hi);
+    scored_span(sc, q0 + i, ctx - q_len + i, ctx, lo, hi);
     const RowParts parts = row_parts(lo, hi, base, p.partition_size);
     if (parts.direct()) continue;  // written by the attention kernel
     const size_t row = (size_t)(q0 + i) * p.num_heads + h;
@@ -39,6 +38,68 @@ __global__ void __launch_bounds__(32 * kReduceRows)
     reduce_load_row<D>(p.part_o, p.part_m, p.part_l, at, p.max_partitions - parts.first, lane, mp, lp, o_early);
     reduce_combine_row<T, D>(static_cast<T*>(p.out), p.part_o, p.part_m, p.part_l, at, row,
                              parts.last - parts.first + 1, mp, lp, o_early, lane);
+  }
+}
+
+// The same for drafted trees: a warp per (query token, head), per_cta query tokens of a sequence a CTA, so that few
+// rows of many partitions (one long context) still fill the GPU; eight partials in flight.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kReduceRows)
+    pkv_tree_reduce_kernel(const DecodeParams p, const ScoreParams sc, int per_cta) {
+  pdl_begin();
+  constexpr int DPL = D / 32, BATCH = 8;
+  const int s = blockIdx.x, h = blockIdx.y * kReduceRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (h >= p.num_heads) return;
+  const int c = p.context_lens[s];
+  const int ctx = c < 0 ? 0 : (c > p.ctx_limit ? p.ctx_limit : c);
+  int q0 = 0;
+  const int q_len = scored_query_len(sc, s, ctx, q0);
+  const int first = (int)blockIdx.z * per_cta;
+  for (int i = first; i < min(q_len, first + per_cta); ++i) {
+    int lo, hi;
+    scored_span<true>(sc, q0 + i, 0, ctx, lo, hi);
+    const RowParts parts = row_parts(lo, hi, 0, p.partition_size);
+    if (parts.direct()) continue;  // written by the attention kernel
+    const size_t row = (size_t)(q0 + i) * p.num_heads + h, at = row * p.max_partitions + parts.first;
+    const int np = parts.last - parts.first + 1;
+    float M = -INFINITY;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, p.part_m[at + k]);
+    M = warp_max(M);
+    float acc[DPL], W = 0.f;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < np; k0 += 32) {
+      float w = 0.f;  // lane k: the weight of partial k0 + k
+      if (k0 + lane < np) {
+        const float m = p.part_m[at + k0 + lane];
+        w = m == -INFINITY ? 0.f : p.part_l[at + k0 + lane] * fast_exp2(m - M);
+      }
+      W += w;
+      for (int k = 0; k < min(32, np - k0); k += BATCH) {
+        float o[BATCH][DPL];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+          for (int e = 0; e < DPL; e += 2) {
+            const float2 v = k0 + k + b < np ? *reinterpret_cast<const float2*>(p.part_o + (at + k0 + k + b) * D +
+                                                                                lane * DPL + e)
+                                             : make_float2(0.f, 0.f);
+            o[b][e] = v.x;
+            o[b][e + 1] = v.y;
+          }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const float wb = __shfl_sync(kFull, w, k + b);
+#pragma unroll
+          for (int e = 0; e < DPL; ++e) acc[e] = fmaf(wb, o[b][e], acc[e]);
+        }
+      }
+    }
+    W = warp_sum(W);
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * DPL);
+#pragma unroll
+    for (int e = 0; e < DPL / 2; ++e) dst[e] = Elem<T>::pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   }
 }
 
@@ -106,6 +167,60 @@ ScoredPlan scored_plan(bool fp8, int num_query_tokens, int num_heads, int num_kv
   const long long np = (span + pl.P - 1) / pl.P;
   pl.np = np < 1 ? 1 : (int)np;
   pl.partials = pl.np > 1 ? (size_t)num_query_tokens * num_heads * pl.np * (head_dim + 2) * sizeof(float) : 0;
+  return pl;
+}
+
+// Tree attention: the tensor-memory tile (128 rows a CTA) from the second 8-column tile on. Measured, us a call, 8-column
+// and tensor tile, 64 contexts of 1000 to 3000 tokens, 32/8 heads: 16-bit pool 8 rows 110, 109; 12 rows 119, 107; 16 rows
+// 126, 111; 32 rows 210, 113; head_dim 64: 8 rows 67, 72; 12 rows 97, 76; E4M3: 8 rows 72, 97; 12 rows 106, 97; 32 rows
+// 199, 101; 4 contexts of 9001 to 32768, 40 heads: 8 rows 298, 352; 24 rows 407, 307.
+constexpr int kTreeTensorRows = 9, kTreeRowTile = 128;
+constexpr int kTreeSms = 152;
+// What a call takes in n equal partitions a sequence, us, if every context is of max_context_len: rounds of CTAs, each a
+// partition's 64-token tiles and an item's start and end, then the partials' way through memory and the reduce kernel.
+// (Measured per tile and item: 16-bit 0.75 and 3, E4M3 0.51 and 6; head_dim 64 about half a tile.) One long context of
+// 32768 tokens, 32/8 heads: 12 to 19 partitions 45, 6 60, 3 103; 4 contexts of 16384, 40 heads: 1 336, 4 248, 6 244, 12
+// 257; 64 contexts to 2048, 32/8 heads: 1 76, 2 105.
+float tree_cost(bool fp8, int head_dim, long long items, long long rows, long long span, long long n) {
+  const float tile = head_dim == 64 ? 0.4f : fp8 ? 0.51f : 0.75f, item = fp8 ? 6.f : 3.f;
+  const long long tiles = (span + n * 64 - 1) / (n * 64), rounds = (items * n + kTreeSms - 1) / kTreeSms;
+  const float bytes = n > 1 ? (float)rows * n * (head_dim + 2) * 8 : 0.f;
+  return (float)rounds * (tiles * tile + item) + (n > 1 ? 6.f + bytes / 4.5e6f : 0.f);
+}
+
+ScoredPlan tree_plan(bool fp8, int num_query_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                     int max_query_len, int max_context_len, int partition_size, size_t workspace_bytes = SIZE_MAX) {
+  const long long rows = (long long)max_query_len * (num_heads / num_kv_heads);
+  if (rows < kTreeTensorRows)
+    return scored_plan(fp8, num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                       max_context_len, 0, partition_size, workspace_bytes);
+  ScoredPlan pl{};
+  pl.tensor = true;
+  pl.row_tiles = (int)((rows + kTreeRowTile - 1) / kTreeRowTile);
+  const long long span = max_context_len;
+  const size_t one = (size_t)num_query_tokens * num_heads * (head_dim + 2) * sizeof(float);
+  if (partition_size) {
+    pl.P = partition_size;
+  } else {
+    // (the batch has at least num_query_tokens / max_query_len sequences; partitions of at least 256 tokens)
+    const long long seqs = ((long long)num_query_tokens + max_query_len - 1) / max_query_len;
+    const long long items = seqs * num_kv_heads * pl.row_tiles;
+    long long most = span / 256 < 64 ? span / 256 : 64, n = 1;
+    if (one && workspace_bytes / one < (size_t)most) most = (long long)(workspace_bytes / one);
+    float best = INFINITY;
+    for (long long k = 1; k <= (most > 1 ? most : 1); ++k) {
+      const float cost = tree_cost(fp8, head_dim, items, (long long)num_query_tokens * num_heads, span, k);
+      if (cost < best) {
+        best = cost;
+        n = k;
+      }
+    }
+    const long long P = ((span + n - 1) / n + block_size - 1) / block_size * block_size;
+    pl.P = P < block_size ? block_size : (int)P;
+  }
+  const long long np = (span + pl.P - 1) / pl.P;
+  pl.np = np < 1 ? 1 : (int)np;
+  pl.partials = pl.np > 1 ? one * pl.np : 0;
   return pl;
 }
 
@@ -185,9 +300,12 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
     return fail(PKV_ERR_UNSUPPORTED, "pool rows num_blocks * num_kv_heads * block_size must be < 2^31");
   if ((long long)c.num_query_tokens * c.num_heads >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "num_query_tokens * num_heads must be < 2^31");
-  const ScoredPlan pl = scored_plan(c.fp8, c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
-                                    c.max_query_len, c.max_context_len, c.window, c.partition_size,
-                                    c.workspace ? c.workspace_bytes : 0);
+  const size_t room = c.workspace ? c.workspace_bytes : 0;
+  const ScoredPlan pl =
+      c.tree ? tree_plan(c.fp8, c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
+                         c.max_query_len, c.max_context_len, c.partition_size, room)
+             : scored_plan(c.fp8, c.num_query_tokens, c.num_heads, c.num_kv_heads, c.head_dim, c.block_size,
+                           c.max_query_len, c.max_context_len, c.window, c.partition_size, room);
   if ((long long)pl.np * pl.row_tiles >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "partitions * row tiles must be < 2^31");
   // A CTA of the tensor tile looks through the grid for rows, some 0.6 us an empty place (measured: 65536 places for 64
@@ -248,6 +366,10 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   sc.row_tiles = pl.row_tiles;
   sc.tree_mask = reinterpret_cast<const uint32_t*>(c.tree_mask);
   sc.mask_words = c.mask_words;
+  // (a batch of which every CTA takes but one item starts all of them at once)
+  if (c.tree && pl.tensor && c.num_seqs <= kTreeSortSeqs &&
+      (long long)pl.np * pl.row_tiles * c.num_kv_heads * c.num_seqs > kTreeSms)
+    sc.sort_seqs = c.num_seqs;
   if (c.softcap > 0.f) {
     sc.cap_in = scale / c.softcap;
     sc.cap_out = c.softcap * 1.4426950408889634f;
@@ -279,20 +401,26 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
               : scored_cols_16(p, sc, kmap, vmap, f16, c.head_dim, c.block_size, c.num_seqs, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
   if (pl.np > 1) {
-    const dim3 grid((unsigned)c.num_seqs, (unsigned)((c.num_heads + kReduceRows - 1) / kReduceRows),
-                    (unsigned)((c.max_query_len + kReduceTokens - 1) / kReduceTokens));
-    auto reduce = [&](auto kern) {
+    const unsigned head_groups = (unsigned)((c.num_heads + kReduceRows - 1) / kReduceRows);
+    // (trees: up to kTreeReduceCtas CTAs before a CTA takes several query tokens)
+    const long long ctas = (long long)c.num_seqs * head_groups * c.max_query_len;
+    const int per_cta = c.tree ? (int)(ctas > 8ll * kTreeReduceCtas ? 8 : (ctas + kTreeReduceCtas - 1) / kTreeReduceCtas)
+                               : kReduceTokens;
+    const dim3 grid((unsigned)c.num_seqs, head_groups, (unsigned)((c.max_query_len + per_cta - 1) / per_cta));
+    auto scored = [&](auto kern) {
       return launch_kernel(kern, grid, dim3(32 * kReduceRows), 0, c.stream, p, sc, (int)c.block_size);
     };
-    auto of_tree = [&](auto tree) {
-      constexpr bool TREE = decltype(tree)::value;
-      if (c.head_dim == 128)
-        return f16 ? reduce(pkv_scored_reduce_kernel<__half, 128, TREE>)
-                   : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 128, TREE>);
-      return f16 ? reduce(pkv_scored_reduce_kernel<__half, 64, TREE>)
-                 : reduce(pkv_scored_reduce_kernel<__nv_bfloat16, 64, TREE>);
+    auto tree = [&](auto kern) {
+      return launch_kernel(kern, grid, dim3(32 * kReduceRows), 0, c.stream, p, sc, per_cta);
     };
-    e = c.tree ? of_tree(std::true_type{}) : of_tree(std::false_type{});
+    if (c.tree && c.head_dim == 128)
+      e = f16 ? tree(pkv_tree_reduce_kernel<__half, 128>) : tree(pkv_tree_reduce_kernel<__nv_bfloat16, 128>);
+    else if (c.tree)
+      e = f16 ? tree(pkv_tree_reduce_kernel<__half, 64>) : tree(pkv_tree_reduce_kernel<__nv_bfloat16, 64>);
+    else if (c.head_dim == 128)
+      e = f16 ? scored(pkv_scored_reduce_kernel<__half, 128>) : scored(pkv_scored_reduce_kernel<__nv_bfloat16, 128>);
+    else
+      e = f16 ? scored(pkv_scored_reduce_kernel<__half, 64>) : scored(pkv_scored_reduce_kernel<__nv_bfloat16, 64>);
     if (e != cudaSuccess) return cuda_fail(e, "scored reduce launch");
   }
   return PKV_OK;
@@ -384,8 +512,17 @@ pkv_status_t paged_attention_multi_query_scored_fp8(
 size_t paged_attention_tree_workspace_size(int32_t num_query_tokens, int32_t num_heads, int32_t num_kv_heads,
                                            int32_t head_dim, int32_t block_size, int32_t max_query_len,
                                            int32_t max_context_len, int32_t partition_size) {
-  return paged_attention_scored_workspace_size(num_query_tokens, num_heads, num_kv_heads, head_dim, block_size,
-                                               max_query_len, max_context_len, 0, partition_size);
+  if (num_query_tokens <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
+      block_size <= 0 || max_query_len <= 0 || max_context_len < 0 || partition_size < 0)
+    return 0;
+  size_t bytes = 0;  // for either type of pool
+  for (bool fp8 : {false, true}) {
+    const size_t n = tree_plan(fp8, num_query_tokens, num_heads, num_kv_heads, head_dim, block_size, max_query_len,
+                               max_context_len, partition_size)
+                         .partials;
+    if (n > bytes) bytes = n;
+  }
+  return bytes;
 }
 
 pkv_status_t paged_attention_tree(void* out, const void* query, const void* key_cache, const void* value_cache,

@@ -27,7 +27,10 @@ struct ScoreParams {
   int row_tiles = 1;                    // row tiles per (partition, kv head, sequence)
   const uint32_t* tree_mask = nullptr;  // [query tokens][mask_words], of the kernels for trees (TREE)
   int mask_words = 0;
+  int sort_seqs = 0;                    // tree, tensor-memory tile: num_seqs to take them longest first, else 0
 };
+
+constexpr int kTreeSortSeqs = 128;  // sequences that a CTA of the tree's tensor-memory tile can sort
 
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;

@@ -270,7 +270,7 @@ struct ScoredItem {
 };
 
 // The item of CTA (x, y, z) of the grid, on one warp. ntile = -2: nothing to do.
-template <int BS, int NT, bool TREE>
+template <int BS, int NT>
 __device__ __forceinline__ ScoredItem scored_item(const DecodeParams& p, const ScoreParams& sc, int x, int y, int z,
                                                   int lane) {
   ScoredItem m;
@@ -296,12 +296,12 @@ __device__ __forceinline__ ScoredItem scored_item(const DecodeParams& p, const S
   int a = INT32_MAX, b = 0;
   if (!sc.key_begin && !sc.key_end) {  // the first token's first, the last token's last
     int unused;
-    scored_span<TREE>(sc, 0, p0 + ta, m.ctx, a, unused);
-    scored_span<TREE>(sc, 0, p0 + tb, m.ctx, unused, b);
+    scored_span(sc, 0, p0 + ta, m.ctx, a, unused);
+    scored_span(sc, 0, p0 + tb, m.ctx, unused, b);
   } else {
     for (int t = ta + lane; t <= tb; t += 32) {
       int lo, hi;
-      scored_span<TREE>(sc, m.q0 + t, p0 + t, m.ctx, lo, hi);
+      scored_span(sc, m.q0 + t, p0 + t, m.ctx, lo, hi);
       if (hi > lo) {
         a = min(a, lo);
         b = max(b, hi);
@@ -429,7 +429,7 @@ __device__ __forceinline__ bool rows_agree(bool yes) {
   return r != 0;
 }
 
-template <typename T, int D, int BS, bool F8, bool CAP, bool BIAS, bool TREE>
+template <typename T, int D, int BS, bool F8, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     pkv_scored_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ ScoreParams sc,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           __syncwarp();
         }
         if (have)
-          m = scored_item<BS, NT, TREE>(p, sc, x, y, z, lane);
+          m = scored_item<BS, NT>(p, sc, x, y, z, lane);
         else
           m.ntile = -1;  // (nothing is asked again)
         have = false;
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       const bool active = orow >= 0;
       const int pos = m.ctx - m.q_len + ti;
       int lo = 0, hi = 0;
-      if (active) scored_span<TREE>(sc, m.q0 + ti, pos, m.ctx, lo, hi);
+      if (active) scored_span(sc, m.q0 + ti, pos, m.ctx, lo, hi);
       const int base = scored_base(sc, m.ctx, m.q_len, BS);
       const int tok0 = base + m.part * P;
       const RowParts parts = row_parts(lo, hi, base, P);
@@ -838,14 +838,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           const int th = tb + hf * 64;
-          uint32_t nodes[2] = {0u, 0u};  // TREE: the half's keys in the mask of the row's tree (read before the wait)
-          const bool drafted = TREE && th + 64 > m.ctx - m.q_len;
-          if constexpr (TREE) {
-            if (drafted) {
-              nodes[0] = tree_bits(sc, m.q0 + ti, th - (m.ctx - m.q_len));
-              nodes[1] = tree_bits(sc, m.q0 + ti, th + 32 - (m.ctx - m.q_len));
-            }
-          }
           // (tensor-memory accesses are warp-wide: a warp leaves the loop as a whole)
           ok = __all_sync(kFull, tc_wait(s_full + 2 * w + hf, cnt & 1, abort));
           if (!ok) break;
@@ -862,7 +854,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll
             for (int u = 0; u < 32; ++u) x[u] = mul2(x[u], pair2(cap_in, cap_in));
           }
-          const bool whole = !edge && th >= lo && th + 64 <= hi && !drafted;
+          const bool whole = !edge && th >= lo && th + 64 <= hi;
           float f = 1.f;      // factor of what the row holds
           bool resc = false;  // O's row holds terms to rescale
           // The reference m moves, and the row is rescaled, only when a score exceeds it by more than 8, so
@@ -887,12 +879,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 for (int b = 0; b < 32 / BS; ++b)
                   if (!((blocks >> (hf * (NBT / 2) + i * (32 / BS) + b)) & 1u))
                     see[i] &= ~((BS == 32 ? 0xffffffffu : (1u << (BS & 31)) - 1u) << (b * BS));
-            }
-            if constexpr (TREE) {
-              if (drafted) {
-                see[0] &= nodes[0];
-                see[1] &= nodes[1];
-              }
             }
           };
           const bool all_whole = __all_sync(kFull, whole);
@@ -1119,13 +1105,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         }
         // Rows that came out non-finite by a masked key's value (not by NaN scores of their own): again, on the
         // whole warp. A value that a row sees is its own, so a NaN in the cache costs one look over the item's values.
-        uint32_t redo = __ballot_sync(kFull, mine && !fine && ok && l == l &&
-                                                   (lo > m.c0 || hi < m.c1 || (TREE && m.c1 > m.ctx - m.q_len)));
+        uint32_t redo = __ballot_sync(kFull, mine && !fine && ok && l == l && (lo > m.c0 || hi < m.c1));
         if (redo) {
           int bad0, bad1;
           bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1);
-          redo &= __ballot_sync(kFull, bad0 > bad1 || lo > bad0 || hi <= bad1 ||
-                                             (TREE && bad1 >= m.ctx - m.q_len));
+          redo &= __ballot_sync(kFull, bad0 > bad1 || lo > bad0 || hi <= bad1);
         }
         for (; redo; redo &= redo - 1) {
           const int src = __ffs(redo) - 1;
@@ -1134,7 +1118,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           const int at = __shfl_sync(kFull, orow, src);
           const bool rdirect = __shfl_sync(kFull, (int)direct, src);
           float rm, rl, o[D / 32];
-          scored_row<T, C, D, TREE>(p, sc, at, m.s, rh, TREE ? m.ctx - m.q_len : rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o);
+          scored_row<T, C, D>(p, sc, at, m.s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o);
           store_row<T, D>(p, at, m.part, rdirect, lane, rm, rl, o);
         }
       }
@@ -1156,11 +1140,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   }
 }
 
-template <typename T, int D, int BS, bool F8, bool CAP, bool BIAS, bool TREE = false>
+template <typename T, int D, int BS, bool F8, bool CAP, bool BIAS>
 cudaError_t launch_scored_tc_mode(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int num_seqs, cudaStream_t stream) {
   using Sh = ScoredTcShape<T, D, BS, F8>;
-  auto kern = pkv_scored_tc_kernel<T, D, BS, F8, CAP, BIAS, TREE>;
+  auto kern = pkv_scored_tc_kernel<T, D, BS, F8, CAP, BIAS>;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1186,14 +1170,6 @@ cudaError_t launch_scored_tc(const DecodeParams& p, const ScoreParams& sc, const
                      : launch_scored_tc_mode<T, D, BS, F8, true, false>(p, sc, kmap, vmap, num_seqs, stream);
   return sc.slopes ? launch_scored_tc_mode<T, D, BS, F8, false, true>(p, sc, kmap, vmap, num_seqs, stream)
                    : launch_scored_tc_mode<T, D, BS, F8, false, false>(p, sc, kmap, vmap, num_seqs, stream);
-}
-
-// The same over the drafted tokens of a tree.
-template <typename T, int D, int BS, bool F8>
-cudaError_t launch_tree_tc(const DecodeParams& p, const ScoreParams& sc, const CUtensorMap& kmap,
-                           const CUtensorMap& vmap, int num_seqs, cudaStream_t stream) {
-  return sc.cap_out != 0.f ? launch_scored_tc_mode<T, D, BS, F8, true, false, true>(p, sc, kmap, vmap, num_seqs, stream)
-                           : launch_scored_tc_mode<T, D, BS, F8, false, false, true>(p, sc, kmap, vmap, num_seqs, stream);
 }
 
 }  // namespace pkv
