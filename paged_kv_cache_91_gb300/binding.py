@@ -520,6 +520,16 @@ def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int) -> None:
         raise PagedKVError(-1, f"{name} must be contiguous")
 
 
+def _expect_all(dtype: torch.dtype, dev: int, names: str, *tensors) -> None:
+    """Each tensor must be contiguous, of this type and on CUDA device dev (names: theirs, for the message)."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            for name, x in zip(names.split(), tensors):
+                if not x.is_cuda:
+                    raise PagedKVError(-1, f"{name} must be a CUDA tensor")
+                _expect(name, x, dtype, dev)
+
+
 def _run_on(dev: int, stream, fn, args) -> None:
     """fn(*args, stream handle) with device dev current (the library launches on the current device)."""
     if stream is not None:
@@ -776,11 +786,14 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
     dev = query.get_device()
     if dt is None or dev < 0:
         _cuda16("query", query)
-        raise PagedKVError(-1, "query must be a CUDA tensor")
-    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if fp8:
-            _cuda_fp8(n, t)
-        _expect(n, t, t.dtype if fp8 else dtype, dev)
+    if fp8:
+        _cuda_fp8("key_cache", key_cache)
+        _cuda_fp8("value_cache", value_cache)
+        _expect_all(key_cache.dtype, dev, "key_cache", key_cache)
+        _expect_all(value_cache.dtype, dev, "value_cache", value_cache)
+        _expect_all(dtype, dev, "query_out", query_out)
+    else:
+        _expect_all(dtype, dev, "key_cache value_cache query_out", key_cache, value_cache, query_out)
     pool, shape = key_cache.shape, query.shape
     if len(pool) != 4 or len(shape) != 3 or value_cache.shape != pool:
         raise PagedKVError(-1, "the caches must be [blocks][kv heads][block size][head dim], query [tokens][heads][head "
@@ -789,12 +802,19 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
     T, H, D2 = shape
     if D2 != D:
         raise PagedKVError(-1, f"head dim {D2} of query, {D} of the caches")
-    strides = (_qkv_rows("query", query, dtype, dev, T, H, D), _qkv_rows("key", key, dtype, dev, T, Hkv, D),
-               _qkv_rows("value", value, dtype, dev, T, Hkv, D))
-    _expect("query_out", query_out, dtype, dev)
     if query_out.shape != shape:
         raise PagedKVError(-1, "query_out must have query's shape")
-    _expect("slot_mapping", slot_mapping, torch.int64, dev)
+    kv = (T, Hkv, D)
+    qs, ks, vs = query.stride(), key.stride(), value.stride()
+    if (T < 2 or H < 2 or Hkv < 2 or key.shape != kv or value.shape != kv or key.dtype is not dtype
+            or value.dtype is not dtype or key.get_device() != dev or value.get_device() != dev
+            or qs[1:] != (D, 1) or ks[1:] != (D, 1) or vs[1:] != (D, 1)):
+        q_step, k_step, v_step = (_qkv_rows("query", query, dtype, dev, T, H, D),
+                                  _qkv_rows("key", key, dtype, dev, T, Hkv, D),
+                                  _qkv_rows("value", value, dtype, dev, T, Hkv, D))
+    else:
+        q_step, k_step, v_step = qs[0], ks[0], vs[0]
+    _expect_all(torch.int64, dev, "slot_mapping", slot_mapping)
     if slot_mapping.shape != (T,):
         raise PagedKVError(-1, "slot_mapping must have one entry per token")
     at = angles = qw = kw = None
@@ -802,26 +822,26 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
     if (positions is None) != (cos_sin is None):
         raise PagedKVError(-1, "positions and cos_sin go together")
     if cos_sin is not None:
-        _expect("positions", positions, torch.int32, dev)
-        _expect("cos_sin", cos_sin, torch.float32, dev)
+        _expect_all(torch.int32, dev, "positions", positions)
+        _expect_all(torch.float32, dev, "cos_sin", cos_sin)
         if positions.shape != (T,) or cos_sin.dim() != 2:
             raise PagedKVError(-1, "positions must have one entry per token, cos_sin be [max_position][rotary_dim]")
         most, rotary = cos_sin.shape
         at, angles = positions.data_ptr(), cos_sin.data_ptr()
     if q_weight is not None:
-        _expect("q_weight", q_weight, torch.float32, dev)
+        _expect_all(torch.float32, dev, "q_weight", q_weight)
         if q_weight.shape != (D,):
             raise PagedKVError(-1, "q_weight must have one entry per dim of a head")
         qw = q_weight.data_ptr()
     if k_weight is not None:
-        _expect("k_weight", k_weight, torch.float32, dev)
+        _expect_all(torch.float32, dev, "k_weight", k_weight)
         if k_weight.shape != (D,):
             raise PagedKVError(-1, "k_weight must have one entry per dim of a head")
         kw = k_weight.data_ptr()
     _run_on(dev, stream, lib.paged_kv_write_rope_fp8 if fp8 else lib.paged_kv_write_rope,
             (query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
              value_cache.data_ptr(), slot_mapping.data_ptr(), at, angles, most, rotary, 1 if interleaved else 0, qw, kw,
-             eps, T, *strides, H, Hkv, D, B, NB, dt, *scales))
+             eps, T, q_step, k_step, v_step, H, Hkv, D, B, NB, dt, *scales))
     return query_out
 
 
@@ -862,12 +882,9 @@ def paged_kv_tree_layout(parents: torch.Tensor, query_start_loc: torch.Tensor, c
     synchronises the call's stream.
     """
     lib = _lib or load()
-    _cuda_i32("parents", parents)
     dev = parents.get_device()
-    i32 = torch.int32
-    for n, t in (("parents", parents), ("query_start_loc", query_start_loc), ("context_lens", context_lens),
-                 ("tree_mask", tree_mask), ("positions", positions)):
-        _expect(n, t, i32, dev)
+    _expect_all(torch.int32, dev, "parents query_start_loc context_lens tree_mask positions", parents, query_start_loc,
+                context_lens, tree_mask, positions)
     T, S = parents.numel(), context_lens.numel()
     if parents.shape != (T,) or context_lens.shape != (S,) or query_start_loc.shape != (S + 1,):
         raise PagedKVError(-1, "parents must be [T], context_lens [S] and query_start_loc [S + 1]")
@@ -895,15 +912,16 @@ def _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_
     dev = query.get_device()
     if dt is None or dev < 0 or not query.is_contiguous():
         _cuda16("query", query)
-    _expect("out", out, dtype, dev)
-    for n, t in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if fp8:
-            _cuda_fp8(n, t)
-        _expect(n, t, t.dtype if fp8 else dtype, dev)
-    i32 = torch.int32
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start_loc", query_start_loc),
-                 ("tree_mask", tree_mask)):
-        _expect(n, t, i32, dev)
+    if fp8:
+        _cuda_fp8("key_cache", key_cache)
+        _cuda_fp8("value_cache", value_cache)
+        _expect_all(key_cache.dtype, dev, "key_cache", key_cache)
+        _expect_all(value_cache.dtype, dev, "value_cache", value_cache)
+        _expect_all(dtype, dev, "out", out)
+    else:
+        _expect_all(dtype, dev, "out key_cache value_cache", out, key_cache, value_cache)
+    _expect_all(torch.int32, dev, "block_tables context_lens query_start_loc tree_mask", block_tables, context_lens,
+                query_start_loc, tree_mask)
     shape, pool, tables = query.shape, key_cache.shape, block_tables.shape
     if len(pool) != 4 or len(shape) != 3 or len(tables) != 2:
         raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim], query [rows][heads][head "
@@ -924,7 +942,7 @@ def _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_
         max_context_len = maxb * B
     begin = None
     if key_begin is not None:
-        _expect("key_begin", key_begin, i32, dev)
+        _expect_all(torch.int32, dev, "key_begin", key_begin)
         if key_begin.shape != (T,):
             raise PagedKVError(-1, "key_begin must have one entry per query row")
         begin = key_begin.data_ptr()
@@ -993,10 +1011,8 @@ def paged_kv_compact_accepted(key_cache: torch.Tensor, value_cache: torch.Tensor
     pool = key_cache.shape
     if len(pool) not in (4, 5) or value_cache.shape != pool:
         raise PagedKVError(-1, "the caches must both be [blocks][kv heads][block size][head dim], or that per layer")
-    i32 = torch.int32
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start_loc", query_start_loc),
-                 ("accepted", accepted), ("num_accepted", num_accepted)):
-        _expect(n, t, i32, dev)
+    _expect_all(torch.int32, dev, "block_tables context_lens query_start_loc accepted num_accepted", block_tables,
+                context_lens, query_start_loc, accepted, num_accepted)
     layers = pool[0] if len(pool) == 5 else 1
     NB, Hkv, B, D = pool[-4:]
     if block_tables.dim() != 2 or accepted.dim() != 2:

@@ -3,13 +3,16 @@
 //
 // Per row x of D values (a token's head), with w and the token's angles c, s:
 //   y = x * rsqrt(mean(x^2) + eps) * w,  (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s) for the pairs of the rotary dims
-// D / 8 lanes hold a row, 8 consecutive dims (16 bytes) each, so a warp moves whole 128- or 256-byte rows. With halves
-// paired (i, i + R / 2) a lane's partners are all in one other lane (R / 2 is a multiple of 8): one shuffle a value.
+// D / 8 lanes hold a row, two groups of 4 consecutive dims (8 bytes) each. Where halves are paired, (i, i + R / 2), a
+// lane of the first R / 8 takes the dims 4 c .. and R / 2 + 4 c .., so that both of a pair are its own: no exchange, and
+// four cosines and sines for its eight dims. The other lanes, and all of them where neighbours are paired, take eight
+// dims in a row.
 #include <math.h>
 #include <stdint.h>
 
 #include "paged_kv.h"
 #include "pkv_common.cuh"
+#include "pkv_f32x2.cuh"
 #include "pkv_internal.h"
 
 namespace pkv {
@@ -33,65 +36,131 @@ struct RopeParams {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;   // rows that a thread has in flight
+constexpr int kRopeUnroll = 4;   // query rows that a thread has in flight
+constexpr int kRopeCtas = 8;     // CTAs an SM holds (64 registers a thread)
 constexpr int kRopeFill = 608;   // CTAs that fill the GPU: four an SM
 
+// A lane's part of a 16-bit row: its two groups of four dims.
+struct Part {
+  uint2 a, b;
+};
+
+__device__ __forceinline__ Part load_part(const unsigned char* row, int da, int db) {
+  return {__ldg(reinterpret_cast<const uint2*>(row + da * 2)), __ldg(reinterpret_cast<const uint2*>(row + db * 2))};
+}
+__device__ __forceinline__ void store_part(unsigned char* row, int da, int db, const Part& y) {
+  *reinterpret_cast<uint2*>(row + da * 2) = y.a;
+  *reinterpret_cast<uint2*>(row + db * 2) = y.b;
+}
+
 template <typename T>
-__device__ __forceinline__ void widen8(const uint4& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ f32x2 widen2(uint32_t w) {
+  const float2 f = Elem<T>::to_float2(w);
+  return pair2(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+  float a, b;
+  unpair2(v, a, b);
+  return Elem<T>::pack2(a, b);
+}
+
+// E4M3(x / scale) of four values, as paged_kv_write_fp8 rounds it.
+__device__ __forceinline__ uint32_t codes4(f32x2 p, f32x2 q, float scale) {
+  float a, b, c, d;
+  unpair2(p, a, b);
+  unpair2(q, c, d);
+  const uint32_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(c, scale), __fdiv_rn(d, scale)), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// What a lane holds for its dims of every row of a token: the norm's weights, and the cosines and sines of its four
+// pairs (halves: as two pairs of pairs; neighbours: one by one).
+struct Turn {
+  f32x2 w[4];
+  bool normed, turned;
+  float4 cs, sn;
+};
+
+__device__ __forceinline__ void load_weights(Turn& t, const float* w, int da, int db) {
+  t.normed = w != nullptr;
+  if (!w) return;
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w + da)), b = __ldg(reinterpret_cast<const float4*>(w + db));
+  t.w[0] = pair2(a.x, a.y);
+  t.w[1] = pair2(a.z, a.w);
+  t.w[2] = pair2(b.x, b.y);
+  t.w[3] = pair2(b.z, b.w);
+}
+
+// The row of which this lane holds y: normed and turned, in fp32. All lanes of the warp take part.
+template <typename T, int D, bool INTERLEAVED>
+__device__ __forceinline__ void norm_and_turn(const Part& y, const Turn& t, float eps, f32x2 (&x)[4]) {
+  x[0] = widen2<T>(y.a.x);
+  x[1] = widen2<T>(y.a.y);
+  x[2] = widen2<T>(y.b.x);
+  x[3] = widen2<T>(y.b.y);
+  if (t.normed) {
+    float s0, s1;
+    unpair2(fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0])))), s0, s1);
+    float sum = s0 + s1;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = Elem<T>::to_float2(w[e]);
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
+    for (int o = 1; o < D / 8; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    const float inv = rsqrtf(sum * (1.f / D) + eps);
+    const f32x2 inv2 = pair2(inv, inv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], inv2), t.w[e]);
+  }
+  if (t.turned) {
+    if constexpr (INTERLEAVED) {
+      const float co[4] = {t.cs.x, t.cs.y, t.cs.z, t.cs.w}, si[4] = {t.sn.x, t.sn.y, t.sn.z, t.sn.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, b;
+        unpair2(x[e], a, b);
+        x[e] = pair2(a * co[e] - b * si[e], b * co[e] + a * si[e]);
+      }
+    } else {
+      const f32x2 co[2] = {pair2(t.cs.x, t.cs.y), pair2(t.cs.z, t.cs.w)};
+      const f32x2 si[2] = {pair2(t.sn.x, t.sn.y), pair2(t.sn.z, t.sn.w)};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const f32x2 a = x[e], b = x[2 + e];
+        x[e] = sub2(mul2(a, co[e]), mul2(b, si[e]));
+        x[2 + e] = fma2(b, co[e], mul2(a, si[e]));
+      }
+    }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(Elem<T>::pack2(x[0], x[1]), Elem<T>::pack2(x[2], x[3]), Elem<T>::pack2(x[4], x[5]),
-                    Elem<T>::pack2(x[6], x[7]));
-}
-
-// E4M3(x / scale), as paged_kv_write_fp8 rounds it.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    w[e] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * e], scale), __fdiv_rn(x[2 * e + 1], scale)),
-                                    __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-// A CTA takes 1 / parts of one token's rows: queries, then keys, then values, a group of D / 8 lanes a row.
+// A CTA takes 1 / parts of one token's rows, a group of D / 8 lanes a row: of the queries, the keys and the values, in
+// loops of their own.
 template <typename T, int D, bool F8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pkv_write_rope_kernel(const RopeParams p) {
   pdl_begin();
   constexpr int LPR = D / 8, RG = kRopeThreads / LPR;  // lanes a row, rows at a time
   const int t = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
-  const int c = threadIdx.x % LPR, d0 = c * 8;
+  const int c = threadIdx.x % LPR;
   const int H = p.num_heads, Hkv = p.num_kv_heads, R = p.rotary_dim;
-  const int rows = H + 2 * Hkv, step = RG * p.parts;
-  const unsigned char* q = p.query + (size_t)t * p.query_stride * 2;
-  const unsigned char* k = p.key + (size_t)t * p.key_stride * 2;
-  const unsigned char* v = p.value + (size_t)t * p.value_stride * 2;
-  auto load = [&](int r) {
-    const unsigned char* src = r < H ? q + (size_t)r * D * 2
-                               : r < H + Hkv ? k + (size_t)(r - H) * D * 2 : v + (size_t)(r - H - Hkv) * D * 2;
-    return __ldg(reinterpret_cast<const uint4*>(src) + c);
-  };
+  Turn turn;
+  turn.turned = c * 8 < R;
+  const int da = INTERLEAVED || !turn.turned ? 8 * c : 4 * c;  // the lane's first dims
+  const int db = da + (INTERLEAVED || !turn.turned ? 4 : R / 2);
+  const int first = part * RG, g = threadIdx.x / LPR, step = RG * p.parts;
+  const unsigned char* q = p.query + ((size_t)t * p.query_stride + (size_t)(first + g) * D) * 2;
+  const unsigned char* k = p.key + ((size_t)t * p.key_stride + (size_t)(first + g) * D) * 2;
+  const unsigned char* v = p.value + ((size_t)t * p.value_stride + (size_t)(first + g) * D) * 2;
   // the first rows load beside the slot and the position, which they do not depend on
-  const int r0 = part * RG + threadIdx.x / LPR;
-  uint4 raw[kRopeUnroll];
+  Part q_in[kRopeUnroll], k_in, v_in;
 #pragma unroll
   for (int u = 0; u < kRopeUnroll; ++u)
-    if (r0 + u * step < rows) raw[u] = load(r0 + u * step);
+    if (first + g + u * step < H) q_in[u] = load_part(q + (size_t)u * step * D * 2, da, db);
+  if (first + g < Hkv) {
+    k_in = load_part(k, da, db);
+    v_in = load_part(v, da, db);
+  }
   const long long slot = __ldg(p.slot_mapping + t);
   const int pos = R ? __ldg(p.positions + t) : 0;
   const bool lost = R && (unsigned)pos >= (unsigned)p.max_position;  // no angles
@@ -100,83 +169,63 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
     if (slot >= p.num_slots) atomicOr(p.err, PKV_DEVERR_SLOT);
     if (lost && slot >= 0) atomicOr(p.err, PKV_DEVERR_CONTEXT);
   }
-  // this lane's angles: of pairs i0 .. (halves: 8 of them, the lane holds one side; interleaved: 4, both sides)
-  const bool turned = d0 < R;
-  const bool second = !INTERLEAVED && d0 >= R / 2;
-  float cs[8], sn[8];
-  if (turned && !lost) {
-    const float* row = p.cos_sin + (size_t)pos * R;
-    if constexpr (INTERLEAVED) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + d0 / 2));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + R / 2 + d0 / 2));
-      cs[0] = a.x; cs[1] = a.y; cs[2] = a.z; cs[3] = a.w;
-      sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
-    } else {
-      const int i0 = second ? d0 - R / 2 : d0;
-      load8(row + i0, cs);
-      load8(row + R / 2 + i0, sn);
-      if (!second)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sn[e] = -sn[e];  // y_a c - y_b s; the other side is y_b c + y_a s
+  turn.cs = turn.sn = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (turn.turned && !lost) {  // of pairs 4 c ..
+    const float4* row = reinterpret_cast<const float4*>(p.cos_sin + (size_t)pos * R);
+    turn.cs = __ldg(row + c);
+    turn.sn = __ldg(row + R / 8 + c);
+  }
+  if (stored) {
+    constexpr int EB = F8 ? 1 : 2;
+    const long long blk = slot / p.block_size, off = slot - blk * p.block_size;
+    const size_t head = (size_t)p.block_size * D * EB;  // bytes between heads of a block
+    const size_t at = ((size_t)blk * Hkv + first + g) * head + (size_t)off * D * EB;
+    unsigned char *kc = p.key_cache + at, *vc = p.value_cache + at;
+    load_weights(turn, p.k_weight, da, db);
+    for (int base = first; base < Hkv; base += step) {
+      const bool mine = base + g < Hkv;
+      f32x2 x[4];
+      norm_and_turn<T, D, INTERLEAVED>(k_in, turn, p.eps, x);
+      if (mine) {
+        if constexpr (F8) {
+          *reinterpret_cast<uint32_t*>(kc + da) = codes4(x[0], x[1], p.k_scale);
+          *reinterpret_cast<uint32_t*>(kc + db) = codes4(x[2], x[3], p.k_scale);
+          *reinterpret_cast<uint32_t*>(vc + da) = codes4(widen2<T>(v_in.a.x), widen2<T>(v_in.a.y), p.v_scale);
+          *reinterpret_cast<uint32_t*>(vc + db) = codes4(widen2<T>(v_in.b.x), widen2<T>(v_in.b.y), p.v_scale);
+        } else {
+          store_part(kc, da, db,
+                     {make_uint2(pack2<T>(x[0]), pack2<T>(x[1])), make_uint2(pack2<T>(x[2]), pack2<T>(x[3]))});
+          store_part(vc, da, db, v_in);
+        }
+      }
+      k += (size_t)step * D * 2;
+      v += (size_t)step * D * 2;
+      kc += step * head;
+      vc += step * head;
+      if (base + step + g < Hkv) {
+        k_in = load_part(k, da, db);
+        v_in = load_part(v, da, db);
+      }
     }
   }
-  const int lane = threadIdx.x & 31;
-  const int partner = (lane & ~(LPR - 1)) | (turned ? (second ? c - R / 16 : c + R / 16) : c);
-  const long long blk = stored ? slot / p.block_size : 0, off = stored ? slot - blk * p.block_size : 0;
+  load_weights(turn, p.q_weight, da, db);
+  unsigned char* out = p.query_out + ((size_t)t * H + first + g) * D * 2;
   // (all threads of a warp go through the same number of rounds, for the shuffles)
-  for (int base = part * RG; base < rows; base += kRopeUnroll * step) {
+  for (int base = first; base < H; base += kRopeUnroll * step) {
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      if (base + u * step >= rows) break;
-      const int r = base + u * step + threadIdx.x / LPR;
-      const bool row = r < rows, is_q = r < H, is_v = r >= H + Hkv;
-      const uint4 x16 = raw[u];
-      if (r + kRopeUnroll * step < rows) raw[u] = load(r + kRopeUnroll * step);
-      float x[8];
-      widen8<T>(x16, x);
-      const float* w = is_q ? p.q_weight : p.k_weight;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      if (w && !is_v) {
-        const float inv = rsqrtf(sum * (1.f / D) + p.eps);
-        float wt[8];
-        load8(w + d0, wt);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wt[e];
-      }
-      if constexpr (INTERLEAVED) {
-        if (turned && !is_v) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = a * cs[e] - b * sn[e];
-            x[2 * e + 1] = b * cs[e] + a * sn[e];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(kFull, x[e], partner);
-          if (turned && !is_v) x[e] = x[e] * cs[e] + other * sn[e];
-        }
-      }
-      if (!row) continue;
-      if (is_q) {
-        const uint4 y = lost ? make_uint4(0u, 0u, 0u, 0u) : pack8<T>(x);
-        reinterpret_cast<uint4*>(p.query_out + ((size_t)t * H + r) * D * 2)[c] = y;
-      } else if (stored) {
-        const int h = is_v ? r - H - Hkv : r - H;
-        unsigned char* pool = is_v ? p.value_cache : p.key_cache;
-        const size_t at = (((size_t)blk * Hkv + h) * p.block_size + off) * D;
-        if constexpr (F8)
-          reinterpret_cast<uint2*>(pool + at)[c] = codes8(x, is_v ? p.v_scale : p.k_scale);
-        else
-          reinterpret_cast<uint4*>(pool + at * 2)[c] = is_v ? x16 : pack8<T>(x);
-      }
+      if (base + u * step >= H) break;
+      const int r = base + u * step + g;
+      const Part y = q_in[u];
+      if (r + kRopeUnroll * step < H) q_in[u] = load_part(q + (size_t)(kRopeUnroll + u) * step * D * 2, da, db);
+      f32x2 x[4];
+      norm_and_turn<T, D, INTERLEAVED>(y, turn, p.eps, x);
+      Part z = {make_uint2(pack2<T>(x[0]), pack2<T>(x[1])), make_uint2(pack2<T>(x[2]), pack2<T>(x[3]))};
+      if (lost) z = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      if (r < H) store_part(out + (size_t)u * step * D * 2, da, db, z);
     }
+    q += (size_t)kRopeUnroll * step * D * 2;
+    out += (size_t)kRopeUnroll * step * D * 2;
   }
 }
 
@@ -288,7 +337,7 @@ pkv_status_t rope_impl(const RopeCall& c) {
   p.v_scale = c.v_scale;
   // a token's rows are shared by several CTAs while those would not fill the GPU
   const int at_once = kRopeThreads / (c.head_dim / 8);
-  const long long rounds = ((long long)c.num_heads + 2 * c.num_kv_heads + at_once - 1) / at_once;
+  const long long rounds = ((long long)(c.num_heads > c.num_kv_heads ? c.num_heads : c.num_kv_heads) + at_once - 1) / at_once;
   long long parts = (kRopeFill + c.num_tokens - 1) / c.num_tokens;
   if (parts > rounds) parts = rounds;
   p.parts = (int)parts;
