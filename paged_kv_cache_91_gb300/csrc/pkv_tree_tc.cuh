@@ -607,21 +607,22 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       auto c0 = [&] { return F8 ? m.c0 : c0_; };
       auto c1 = [&] { return F8 ? m.c1 : c1_; };
       auto ntile = [&] { return F8 ? m.ntile : ntile_; };
-      // which blocks of a tile were copied: lane b < NBT holds block b's test (the copying warp's own)
-      auto load_ok = [&](int t) {
+      // Which blocks of a tile were copied: lane b < NBT holds block b's id, -1 past the last, to put to the copying
+      // warp's own test. (Loaded a tile ahead and tested when it is used: tested at once, the load held the warp up for
+      // 500 of a tile's 2000 cycles.)
+      auto load_id = [&](int t) {
         const int b = c0() / BS + t * NBT + (lane & (NBT - 1));
-        return b < (c1() + BS - 1) / BS &&
-               (unsigned)p.block_tables[(size_t)m.s * p.max_blocks_per_seq + b] < (unsigned)p.num_blocks;
+        return b < (c1() + BS - 1) / BS ? p.block_tables[(size_t)m.s * p.max_blocks_per_seq + b] : -1;
       };
       constexpr uint32_t all = (1u << NBT) - 1u;
       float m_ref = -INFINITY, l = 0.f;
       int n = 0;
-      bool next = w < ntile() && load_ok(w);
+      int next = w < ntile() ? load_id(w) : -1;
 #pragma unroll 1
       for (int t = w; t < ntile(); t += 2, ++n) {
         const int c = cnt + n, b = c & 1;
-        const uint32_t blocks = __ballot_sync(kFull, next) & all;
-        if (t + 2 < ntile()) next = load_ok(t + 2);
+        const uint32_t blocks = __ballot_sync(kFull, (unsigned)next < (unsigned)p.num_blocks) & all;
+        if (t + 2 < ntile()) next = load_id(t + 2);
         const int th = c0() / BS * BS + t * NT;  // position of the tile's first token
         // V rows outside the item's keys, or not copied
         const bool edge = blocks != all || th < c0() || th + NT > c1();
