@@ -44,9 +44,9 @@ struct TreeTcShape {
   static constexpr int OFF_RING = QT;
   static constexpr int OFF_CODES = OFF_RING + NS * TILE;
   static constexpr int OFF_BARS = OFF_CODES + 4 * NC * CODES;
-  // barriers: full[NS], empty[NS], raw[4 NC], codes_free[4 NC]; per stream and buffer s_full, p_full, pv_done; per
-  // stream fin; q_full; items: info_full[2], info_empty[2], next
-  static constexpr int NBARS = 2 * NS + 8 * NC + 12 + 2 + 1 + 5;
+  // barriers: full[NS], done[NS], raw[4 NC], codes_free[4 NC]; per stream and buffer p_full; per stream fin; q_full;
+  // items: info_full[2], info_empty[2], next
+  static constexpr int NBARS = 2 * NS + 8 * NC + 4 + 2 + 1 + 5;
   static constexpr int OFF_NEXT = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;  // the hardware's answer: the next CTA
   static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag
   static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
@@ -223,11 +223,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   constexpr int NT = Sh::NT, NBT = Sh::NBT, NR = Sh::NR, NS = Sh::NS, NC = Sh::NC, ROWS = Sh::ROWS;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::OFF_BARS);
-  uint64_t *full = bars, *empty = bars + NS, *raw = bars + 2 * NS, *codes_free = raw + 4 * NC;
-  uint64_t* s_full = codes_free + 4 * NC;  // [stream][buffer]
-  uint64_t* p_full = s_full + 4;
-  uint64_t* pv_done = s_full + 8;
-  uint64_t* fin = s_full + 12;  // [stream]: everything issued
+  // full: the tile is in its slot. done: its MMAs have read it, so that S (a K slot) is there or O holds its PV (a V
+  // slot): one barrier for all who wait for that, since a commit costs the issuing thread some 90 cycles.
+  uint64_t *full = bars, *done = bars + NS, *raw = bars + 2 * NS, *codes_free = raw + 4 * NC;
+  uint64_t* p_full = codes_free + 4 * NC;  // [stream][buffer]
+  uint64_t* fin = p_full + 4;              // [stream]: everything issued
   uint64_t* q_full = fin + 2;
   uint64_t* info_full = q_full + 1;   // [2]
   uint64_t* info_empty = info_full + 2;
@@ -254,17 +254,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     prefetch_tensormap(&vmap);
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + k, 1);
-      mbar_init(empty + k, 1);
+      mbar_init(done + k, 1);
     }
     for (int k = 0; k < 4 * NC; ++k) {
       mbar_init(raw + k, 1);
       mbar_init(codes_free + k, 1);
     }
-    for (int k = 0; k < 4; ++k) {
-      mbar_init(s_full + k, 1);
-      mbar_init(p_full + k, ROWS);
-      mbar_init(pv_done + k, 1);
-    }
+    for (int k = 0; k < 4; ++k) mbar_init(p_full + k, ROWS);
     for (int k = 0; k < 2; ++k) {
       mbar_init(fin + k, 1);
       mbar_init(info_full + k, 1);
@@ -400,7 +396,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         const int n = __popc(__ballot_sync(kFull, mine));
         const int row = (id * p.num_kv_heads + m.kvh) * BS;  // first pool row of the block
         const int c = stream ? issued[1] : issued[0], i = (2 * stream + kv) * NL + c % NL;
-        if (c >= NL) ok = __all_sync(kFull, tc_wait((F8 ? codes_free : empty) + i, (c / NL - 1) & 1, abort));
+        if (c >= NL) ok = __all_sync(kFull, tc_wait((F8 ? codes_free : done) + i, (c / NL - 1) & 1, abort));
         if (!ok) break;
         if (lane == 0) {
           if (!F8) fence_proxy_async_smem();  // generic stores into the slot (zeroed rows): before the copies
@@ -444,7 +440,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         for (; ok && c < end; ++c) {
           const int from = r * NC + c % NC, to = slot_of(r >> 1, r & 1, c);
           ok = __all_sync(kFull, tc_wait(raw + from, (c / NC) & 1, abort) &&
-                                     (c < NR || tc_wait(empty + to, (c / NR - 1) & 1, abort)));
+                                     (c < NR || tc_wait(done + to, (c / NR - 1) & 1, abort)));
           if (!ok) break;
           tree_widen(slot(to), smem + Sh::OFF_CODES + from * Sh::CODES, lane);
           fence_proxy_async_smem();  // generic stores, read by the MMAs
@@ -463,7 +459,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     constexpr uint32_t IDESC_S = tc::idesc_f16(BF, ROWS, NT, false, false);
     constexpr uint32_t IDESC_O = tc::idesc_f16(BF, ROWS, D, false, true);
     const uint32_t scol = tbase + Sh::S_COL + st * 128, ocol = tbase + Sh::O_COL + st * 128;
-    const uint32_t q_addr = smem_u32(smem);
+    // (descriptors are built once and stepped by constants: one built anew for every MMA kept the issuing thread, which
+    // is what bounds a tile out of L2, for 80 cycles an MMA)
+    const uint64_t q_desc = tc::desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = tc::desc_sw128(smem_u32(slot(slot_of(st, 0, 0))), 16, Sh::ATOM);
+    const uint64_t v_desc = tc::desc_sw128(smem_u32(slot(slot_of(st, 1, 0))), 1024, Sh::ATOM);
     TreeItem m;
     int cnt = 0, nq = 0;  // this stream's tiles and the items with keys before
     bool ok = true;
@@ -475,33 +475,32 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       if (lane == 0) {
         // S of the stream's tile c, once its K has landed and the PV two before has read its P from these columns
         auto issue_s = [&](int c) {
-          const int i = slot_of(st, 0, c), b = c & 1;
+          const int i = slot_of(st, 0, c);
           if (!tc_wait(full + i, phase_of(c), abort)) return false;
-          if (c >= 2 && !tc_wait(pv_done + 2 * st + b, ((c >> 1) - 1) & 1, abort)) return false;
+          if (c >= 2 && !tc_wait(done + slot_of(st, 1, c - 2), phase_of(c - 2), abort)) return false;
           tc::fence_after_sync();
-          const uint32_t k_addr = smem_u32(slot(i));
+          const uint64_t b_desc = k_desc + (uint64_t)((c % NR) * (Sh::TILE / 16));
+          const uint32_t to = scol + (c & 1) * 64;
 #pragma unroll
           for (int u = 0; u < D / 16; ++u)
-            tc::mma_f16(scol + b * 64, tc::desc_sw128(q_addr + (u / 4) * (ROWS * 128) + (u % 4) * 32, 16, 1024),
-                        tc::desc_sw128(k_addr + (u / 4) * 1024 + (u % 4) * 32, 16, Sh::ATOM), IDESC_S, u > 0);
-          tc::commit(s_full + 2 * st + b);
-          tc::commit(empty + i);
+            tc::mma_f16(to, q_desc + ((u / 4) * (ROWS * 128) + (u % 4) * 32) / 16,
+                        b_desc + ((u / 4) * 1024 + (u % 4) * 32) / 16, IDESC_S, u > 0);
+          tc::commit(done + i);
           return true;
         };
         ok = tc_wait(q_full, nq & 1, abort);
         for (int c = cnt; ok && c < min(end, cnt + 2); ++c) ok = issue_s(c);
         for (int c = cnt; ok && c < end; ++c) {
-          const int i = slot_of(st, 1, c), b = c & 1;
-          ok = tc_wait(p_full + 2 * st + b, (c >> 1) & 1, abort) && tc_wait(full + i, phase_of(c), abort);
+          const int i = slot_of(st, 1, c);
+          ok = tc_wait(full + i, phase_of(c), abort) && tc_wait(p_full + 2 * st + (c & 1), (c >> 1) & 1, abort);
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t v_addr = smem_u32(slot(i));
+          const uint64_t b_desc = v_desc + (uint64_t)((c % NR) * (Sh::TILE / 16));
+          const uint32_t from = scol + (c & 1) * 64;
 #pragma unroll
           for (int u = 0; u < NT / 16; ++u)  // 16 keys each: 8 columns of P, two atoms of V
-            tc::mma_f16_ta(ocol, scol + b * 64 + u * 8, tc::desc_sw128(v_addr + u * 2 * Sh::ATOM, 1024, Sh::ATOM),
-                           IDESC_O, c > cnt || u > 0);
-          tc::commit(pv_done + 2 * st + b);
-          tc::commit(empty + i);
+            tc::mma_f16_ta(ocol, from + u * 8, b_desc + u * 2 * Sh::ATOM / 16, IDESC_O, u > 0 || c > cnt);
+          tc::commit(done + i);
           if (c + 2 < end) ok = issue_s(c + 2);
         }
       }
@@ -633,7 +632,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           nodes[1] = tree_bits(sc, m.q0 + ti, th + 32 - node0);
         }
         // (tensor-memory accesses are warp-wide: a warp leaves the loop as a whole)
-        ok = __all_sync(kFull, tc_wait(s_full + 2 * w + b, (c >> 1) & 1, abort));
+        ok = __all_sync(kFull, tc_wait(done + slot_of(w, 0, c), phase_of(c), abort));
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t sr[2][32];
@@ -757,7 +756,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         if (__any_sync(kFull, resc)) {  // the whole warp moves its rows' O (factor 1 for rows that keep theirs)
           // the PV two before is done (its P's columns hold this S); the one before may still be multiplied
           // (a row that moves has seen keys, so there is one)
-          ok = __all_sync(kFull, n == 0 || tc_wait(pv_done + 2 * w + (b ^ 1), ((c - 1) >> 1) & 1, abort));
+          ok = __all_sync(kFull, n == 0 || tc_wait(done + slot_of(w, 1, c - 1), phase_of(c - 1), abort));
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll
@@ -792,7 +791,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       cnt += n;
       // ---- the streams meet: their PVs are done, their (m, l) at hand, and Q's place is free
       if (ok && n > 0)
-        ok = __all_sync(kFull, tc_wait(pv_done + 2 * w + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1, abort));
+        ok = __all_sync(kFull, tc_wait(done + slot_of(w, 1, cnt - 1), phase_of(cnt - 1), abort));
       ml[2 * ROWS * w + row] = n > 0 ? m_ref : -INFINITY;
       ml[2 * ROWS * w + ROWS + row] = n > 0 ? l : 0.f;
       tc::fence_before_sync();
