@@ -520,14 +520,30 @@ def _expect(name: str, t: torch.Tensor, dtype: torch.dtype, dev: int) -> None:
         raise PagedKVError(-1, f"{name} must be contiguous")
 
 
-def _expect_all(dtype: torch.dtype, dev: int, names: str, *tensors) -> None:
-    """Each tensor must be contiguous, of this type and on CUDA device dev (names: theirs, for the message)."""
-    for t in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous():
-            for name, x in zip(names.split(), tensors):
+def _expect_all(dev: int, names: str, tensors, dtypes) -> None:
+    """Each tensor (or None) must be contiguous, of its type and on CUDA device dev (names: theirs, for the message)."""
+    for t, dtype in zip(tensors, dtypes):
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            for name, x, d in zip(names.split(), tensors, dtypes):
+                if x is None:
+                    continue
                 if not x.is_cuda:
                     raise PagedKVError(-1, f"{name} must be a CUDA tensor")
-                _expect(name, x, dtype, dev)
+                _expect(name, x, d, dev)
+
+
+def _pool_dtype(key_cache, value_cache, dtype, fp8):
+    """The caches' type: the queries', or their own 8-bit one."""
+    if not fp8:
+        return dtype
+    if key_cache.dtype not in _FP8_DTYPES or value_cache.dtype is not key_cache.dtype:
+        _cuda_fp8("key_cache", key_cache)
+        _cuda_fp8("value_cache", value_cache)
+        raise PagedKVError(-1, f"value_cache is {value_cache.dtype}, key_cache {key_cache.dtype}")
+    return key_cache.dtype
+
+
+_I32 = (torch.int32,) * 5
 
 
 def _run_on(dev: int, stream, fn, args) -> None:
@@ -786,14 +802,10 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
     dev = query.get_device()
     if dt is None or dev < 0:
         _cuda16("query", query)
-    if fp8:
-        _cuda_fp8("key_cache", key_cache)
-        _cuda_fp8("value_cache", value_cache)
-        _expect_all(key_cache.dtype, dev, "key_cache", key_cache)
-        _expect_all(value_cache.dtype, dev, "value_cache", value_cache)
-        _expect_all(dtype, dev, "query_out", query_out)
-    else:
-        _expect_all(dtype, dev, "key_cache value_cache query_out", key_cache, value_cache, query_out)
+    stored, f32 = _pool_dtype(key_cache, value_cache, dtype, fp8), torch.float32
+    _expect_all(dev, "key_cache value_cache query_out slot_mapping positions cos_sin q_weight k_weight",
+                (key_cache, value_cache, query_out, slot_mapping, positions, cos_sin, q_weight, k_weight),
+                (stored, stored, dtype, torch.int64, torch.int32, f32, f32, f32))
     pool, shape = key_cache.shape, query.shape
     if len(pool) != 4 or len(shape) != 3 or value_cache.shape != pool:
         raise PagedKVError(-1, "the caches must be [blocks][kv heads][block size][head dim], query [tokens][heads][head "
@@ -814,7 +826,6 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
                                   _qkv_rows("value", value, dtype, dev, T, Hkv, D))
     else:
         q_step, k_step, v_step = qs[0], ks[0], vs[0]
-    _expect_all(torch.int64, dev, "slot_mapping", slot_mapping)
     if slot_mapping.shape != (T,):
         raise PagedKVError(-1, "slot_mapping must have one entry per token")
     at = angles = qw = kw = None
@@ -822,19 +833,15 @@ def _write_rope(query_out, query, key, value, key_cache, value_cache, slot_mappi
     if (positions is None) != (cos_sin is None):
         raise PagedKVError(-1, "positions and cos_sin go together")
     if cos_sin is not None:
-        _expect_all(torch.int32, dev, "positions", positions)
-        _expect_all(torch.float32, dev, "cos_sin", cos_sin)
         if positions.shape != (T,) or cos_sin.dim() != 2:
             raise PagedKVError(-1, "positions must have one entry per token, cos_sin be [max_position][rotary_dim]")
         most, rotary = cos_sin.shape
         at, angles = positions.data_ptr(), cos_sin.data_ptr()
     if q_weight is not None:
-        _expect_all(torch.float32, dev, "q_weight", q_weight)
         if q_weight.shape != (D,):
             raise PagedKVError(-1, "q_weight must have one entry per dim of a head")
         qw = q_weight.data_ptr()
     if k_weight is not None:
-        _expect_all(torch.float32, dev, "k_weight", k_weight)
         if k_weight.shape != (D,):
             raise PagedKVError(-1, "k_weight must have one entry per dim of a head")
         kw = k_weight.data_ptr()
@@ -883,8 +890,8 @@ def paged_kv_tree_layout(parents: torch.Tensor, query_start_loc: torch.Tensor, c
     """
     lib = _lib or load()
     dev = parents.get_device()
-    _expect_all(torch.int32, dev, "parents query_start_loc context_lens tree_mask positions", parents, query_start_loc,
-                context_lens, tree_mask, positions)
+    _expect_all(dev, "parents query_start_loc context_lens tree_mask positions",
+                (parents, query_start_loc, context_lens, tree_mask, positions), _I32)
     T, S = parents.numel(), context_lens.numel()
     if parents.shape != (T,) or context_lens.shape != (S,) or query_start_loc.shape != (S + 1,):
         raise PagedKVError(-1, "parents must be [T], context_lens [S] and query_start_loc [S + 1]")
@@ -912,16 +919,10 @@ def _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_
     dev = query.get_device()
     if dt is None or dev < 0 or not query.is_contiguous():
         _cuda16("query", query)
-    if fp8:
-        _cuda_fp8("key_cache", key_cache)
-        _cuda_fp8("value_cache", value_cache)
-        _expect_all(key_cache.dtype, dev, "key_cache", key_cache)
-        _expect_all(value_cache.dtype, dev, "value_cache", value_cache)
-        _expect_all(dtype, dev, "out", out)
-    else:
-        _expect_all(dtype, dev, "out key_cache value_cache", out, key_cache, value_cache)
-    _expect_all(torch.int32, dev, "block_tables context_lens query_start_loc tree_mask", block_tables, context_lens,
-                query_start_loc, tree_mask)
+    stored = _pool_dtype(key_cache, value_cache, dtype, fp8)
+    _expect_all(dev, "out key_cache value_cache block_tables context_lens query_start_loc tree_mask key_begin",
+                (out, key_cache, value_cache, block_tables, context_lens, query_start_loc, tree_mask, key_begin),
+                (dtype, stored, stored, *_I32))
     shape, pool, tables = query.shape, key_cache.shape, block_tables.shape
     if len(pool) != 4 or len(shape) != 3 or len(tables) != 2:
         raise PagedKVError(-1, "key_cache must be [blocks][kv heads][block size][head dim], query [rows][heads][head "
@@ -942,7 +943,6 @@ def _tree(out, query, key_cache, value_cache, block_tables, context_lens, query_
         max_context_len = maxb * B
     begin = None
     if key_begin is not None:
-        _expect_all(torch.int32, dev, "key_begin", key_begin)
         if key_begin.shape != (T,):
             raise PagedKVError(-1, "key_begin must have one entry per query row")
         begin = key_begin.data_ptr()
@@ -1011,8 +1011,8 @@ def paged_kv_compact_accepted(key_cache: torch.Tensor, value_cache: torch.Tensor
     pool = key_cache.shape
     if len(pool) not in (4, 5) or value_cache.shape != pool:
         raise PagedKVError(-1, "the caches must both be [blocks][kv heads][block size][head dim], or that per layer")
-    _expect_all(torch.int32, dev, "block_tables context_lens query_start_loc accepted num_accepted", block_tables,
-                context_lens, query_start_loc, accepted, num_accepted)
+    _expect_all(dev, "block_tables context_lens query_start_loc accepted num_accepted",
+                (block_tables, context_lens, query_start_loc, accepted, num_accepted), _I32)
     layers = pool[0] if len(pool) == 5 else 1
     NB, Hkv, B, D = pool[-4:]
     if block_tables.dim() != 2 or accepted.dim() != 2:
