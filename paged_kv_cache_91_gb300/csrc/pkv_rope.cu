@@ -7,6 +7,12 @@
 // lane of the first R / 8 takes the dims 4 c .. and R / 2 + 4 c .., so that both of a pair are its own: no exchange, and
 // four cosines and sines for its eight dims. The other lanes, and all of them where neighbours are paired, take eight
 // dims in a row.
+//
+// Bound by HBM once the batch is large, with the issue slots close behind (16384 tokens, 32/8 heads, bf16: 72 us, 5.7 TB/s,
+// 84 % of the copy rate; issue 73 %); a step's 256 tokens into an E4M3 pool take 4.7 us replayed from a graph, latency.
+// On the way there (16384 tokens, with the launch, us): eight dims in a row a lane with the partner's values by shuffle 122,
+// pairs within a lane 107, 64 registers a thread for 8 CTAs an SM 98, packed arithmetic and loops of their own for
+// queries, keys and values 88.
 #include <math.h>
 #include <stdint.h>
 
