@@ -206,7 +206,7 @@ __device__ __forceinline__ void tree_fetch_q_bf16_as_f16(unsigned char* Qs, int 
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
     int k = top ? 127 - (int)(top >> 7) : 0;
-    k = max(-100, min(100, k));
+    k = max(-126, min(126, k));
     const float pw = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     uint64_t* landed = F8 ? raw : full;
     constexpr int NL = F8 ? NC : NR;  // slots of a ring where tiles land
     int asked = 0;
+    bool pending = false;  // an answer is on its way
     auto ask = [&] {
       if (lane == 0) {
         fence_proxy_async_smem();  // the answer before has been read
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       }
       __syncwarp();
       ++asked;
+      pending = true;
     };
     // the item of the answer at hand, or of this CTA: as item k, once two before is free; false if it is empty
     auto publish = [&](int k, bool have, int x, int y, int z) {
@@ -348,13 +350,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     bool found = true;
     auto look = [&](int k, bool block) {
       while (ok && !found) {
-        if (block) {
+        if (block)
           ok = __all_sync(kFull, tc_wait(next_bar, (asked - 1) & 1, abort));
-          if (!ok) mbar_wait(next_bar, (asked - 1) & 1);  // (it may not land in a CTA that has left)
-        } else if (!__all_sync(kFull, mbar_test(next_bar, (asked - 1) & 1))) {
+        else if (!__all_sync(kFull, mbar_test(next_bar, (asked - 1) & 1)))
           return;
-        }
         if (!ok) return;
+        pending = false;
         int x, y, z;
         const bool have = next_cta(smem + Sh::OFF_NEXT, x, y, z);
         __syncwarp();
@@ -429,7 +430,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       }
       if (finder) look(k + 1, true);
     }
-    // no copy may still be landing when the CTA leaves
+    // no answer and no copy may still be landing when the CTA leaves
+    if (pending) mbar_wait(next_bar, (asked - 1) & 1);
     if (lane == 0)
       for (int st = 0; st < 2; ++st)
         for (int c = max(0, issued[st] - NL); c < issued[st]; ++c)

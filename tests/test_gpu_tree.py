@@ -1,5 +1,7 @@
 """Attention of drafted trees on the GPU against the definition in 64 bits, within the error that the formats allow
 (tests/tree_reference.py)."""
+import random
+
 import pytest
 import torch
 
@@ -242,3 +244,80 @@ def test_a_long_cache(q):
                                  b["mask"].to(DEV), b["scale"], max_query_len=q)
     torch.cuda.synchronize()
     assert R.worst(out, ref, tol) <= 1.0
+
+
+@pytest.mark.parametrize("H,Hkv,D,B,dtype,fp8", [(16, 8, 128, 16, "bf16", False), (16, 8, 64, 8, "f16", False),
+                                                 (16, 8, 128, 32, "bf16", True), (24, 8, 128, 16, "f16", True)])
+@pytest.mark.parametrize("part", [0, 96])
+def test_more_work_than_ctas(H, Hkv, D, B, dtype, fp8, part):
+    """CTAs that take several items each, sequences of every length in no order: long ones, without drafted tokens, that
+    wait, with nothing committed, with bad offsets."""
+    r = random.Random(45)
+    committed = [r.choice([0, 3, 40, 130, 400, r.randint(0, 300)]) for _ in range(46)]
+    qlens = [r.choice([0, 1, 5, 6, 9]) for _ in committed]
+    qlens[3], qlens[20] = 9, 70  # (several row tiles)
+    b = TR.build(45, committed, qlens, H, Hkv, D, B, dtype, fp8)
+    begin = [0] * sum(qlens)
+    for s in (5, 6, 30, 45):
+        for t in range(b["starts"][s], b["starts"][s + 1]):
+            begin[t] = HIDE
+        b["tables"][s] = -1
+    for s in (7, 8):  # windows
+        for t in range(b["starts"][s], b["starts"][s + 1]):
+            begin[t] = max(0, committed[s] - 20)
+    if part:
+        part = part // B * B
+    ref, tol = TR.reference(b, key_begin=begin)
+    rows = list(range(sum(qlens)))
+    out = torch.full_like(b["q"], 7.0, device=DEV)
+    call(b, key_begin=begin, out=out, partition_size=part)
+    assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
+    bad = next(s for s in range(10, 46) if qlens[s] > 1)
+    b["ctx"][bad] = 1
+    gone = rows[b["starts"][bad]:b["starts"][bad + 1]]
+    keep = [t for t in rows if t not in gone]
+    out.fill_(7.0)
+    call(b, key_begin=begin, out=out, partition_size=part, max_ctx=b["tables"].shape[1] * B)
+    assert R.worst(out[keep], ref[keep], tol[keep]) <= 1.0 and (out[gone] == 7.0).all()
+    assert binding.device_errors() == 16
+
+
+def test_more_sequences_than_are_sorted():
+    r = random.Random(46)
+    committed = [r.randint(0, 60) for _ in range(150)]
+    b = TR.build(46, committed, [r.randint(1, 4) for _ in committed], 12, 4, 128, 16)
+    check(b)
+    check(b, part=32)
+
+
+@pytest.mark.parametrize("q", [2, 20])
+@pytest.mark.parametrize("power", [-50, 50])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+def test_queries_of_any_size(q, power, fp8, softcap):
+    """Queries far from 1 with a scale that brings the scores back, and a row of zeros."""
+    b = TR.build(47, [150, 9], [q, q], 8, 2, 128, 16, fp8=fp8)
+    b["q"] = b["q"] * 2.0 ** power
+    b["q"][1, 3] = 0.0
+    b["scale"] = 128 ** -0.5 * 2.0 ** -power
+    check(b, softcap=softcap)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    bs = [TR.build(s, [700, 300, 40], [24, 30, 12], 8, 2, 128, 16) for s in (48, 49)]
+    dev = [{k: b[k].to(DEV) for k in ("q", "kc", "vc", "tables", "mask")} for b in bs]
+    ctx, starts = [i32(b["ctx"]) for b in bs], [i32(b["starts"]) for b in bs]
+    outs, streams = [torch.empty_like(d["q"]) for d in dev], [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, b in enumerate(bs):
+            d = dev[i]
+            binding.paged_attention_tree(outs[i], d["q"], d["kc"], d["vc"], d["tables"], ctx[i], starts[i], d["mask"],
+                                         b["scale"], max_query_len=30, max_context_len=max(b["ctx"]),
+                                         partition_size=128, stream=streams[i])
+    torch.cuda.synchronize()
+    for b, out in zip(bs, outs):
+        ref, tol = TR.reference(b)
+        assert R.worst(out, ref, tol) <= 1.0
