@@ -483,10 +483,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       if (m.ntile == 0) continue;
       const int end = cnt + m.tiles(st);
       if (lane == 0) {
-        // S of the stream's tile c, once its K has landed and the PV two before has read its P from these columns
+        // (the waits for tiles to land stand where MMAs run meanwhile: a wait costs some 90 cycles also when it is over)
+        auto landed = [&](int kv, int c) { return c >= end || tc_wait(full + slot_of(st, kv, c), phase_of(c), abort); };
+        // S of the stream's tile c, whose K has landed, once the PV two before has read its P from these columns
         auto issue_s = [&](int c) {
           const int i = slot_of(st, 0, c);
-          if (!tc_wait(full + i, phase_of(c), abort)) return false;
           if (c >= 2 && !tc_wait(done + slot_of(st, 1, c - 2), phase_of(c - 2), abort)) return false;
           tc::fence_after_sync();
           const uint64_t b_desc = k_desc + (uint64_t)((c % NR) * (Sh::TILE / 16));
@@ -498,11 +499,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           tc::commit(done + i);
           return true;
         };
-        ok = tc_wait(q_full, nq & 1, abort);
-        for (int c = cnt; ok && c < min(end, cnt + 2); ++c) ok = issue_s(c);
+        ok = landed(0, cnt) && tc_wait(q_full, nq & 1, abort);
+        for (int c = cnt; ok && c < min(end, cnt + 2); ++c) ok = landed(0, c) && issue_s(c);
+        ok = ok && landed(1, cnt);
         for (int c = cnt; ok && c < end; ++c) {
           const int i = slot_of(st, 1, c);
-          ok = tc_wait(full + i, phase_of(c), abort) && tc_wait(p_full + 2 * st + (c & 1), (c >> 1) & 1, abort);
+          ok = tc_wait(p_full + 2 * st + (c & 1), (c >> 1) & 1, abort);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t b_desc = v_desc + (uint64_t)((c % NR) * (Sh::TILE / 16));
@@ -511,7 +513,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           for (int u = 0; u < NT / 16; ++u)  // 16 keys each: 8 columns of P, two atoms of V
             tc::mma_f16_ta(ocol, from + u * 8, b_desc + u * 2 * Sh::ATOM / 16, IDESC_O, u > 0 || c > cnt);
           tc::commit(done + i);
-          if (c + 2 < end) ok = issue_s(c + 2);
+          ok = landed(0, c + 2) && landed(1, c + 1);
+          if (ok && c + 2 < end) ok = issue_s(c + 2);
         }
       }
       cnt = end;
