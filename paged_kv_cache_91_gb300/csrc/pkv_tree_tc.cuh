@@ -24,10 +24,10 @@
 // keys, were slower (E4M3: 0.70 us a tile): what a tile costs a warp besides its keys doubles.
 //
 // Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 copies K, 11 copies V and
-// finds the items; FP8 pool: 12-15 widen the codes of one (stream, K or V) ring each to f16, from the slots where they land to the ring
-// that the MMAs read. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set
-// PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has already claimed for
-// later stay as they were.
+// finds the items; FP8 pool: 12-15 widen the codes of one (stream, K or V) ring each to f16, from the slots where they
+// land to the ring that the MMAs read. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop,
+// set PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has already claimed
+// for later stay as they were.
 #pragma once
 
 #include <type_traits>
@@ -116,6 +116,7 @@ __device__ __forceinline__ TreeItem tree_item(const DecodeParams& p, const Score
   }
   const int G = p.group;
   if (m.row0() >= (long long)m.q_len * G) return m;
+  if (m.part > 0 && m.part * p.partition_size >= m.ctx) return m;
   // its rows' first visible key; the last is the context's
   int a = 0, b = m.ctx;
   if (sc.key_begin) {

@@ -321,3 +321,52 @@ def test_two_calls_at_once():
     for b, out in zip(bs, outs):
         ref, tol = TR.reference(b)
         assert R.worst(out, ref, tol) <= 1.0
+
+
+@pytest.mark.parametrize("H,Hkv,D,B,fp8", [(160, 1, 128, 16, False), (144, 1, 64, 8, False), (300, 2, 128, 32, True)])
+def test_many_heads_a_kv_head(H, Hkv, D, B, fp8):
+    """A token's heads pass a row tile."""
+    b = TR.build(50, [70, 5], [1, 3], H, Hkv, D, B, fp8=fp8)
+    check(b)
+    check(b, part=64, softcap=3.0)
+
+
+@pytest.mark.parametrize("part", [0, 64])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_loose_bounds(fp8, part):
+    """Bounds on query tokens and contexts far above what there is: row tiles and partitions without work."""
+    b = TR.build(51, [0, 300, 21], [2, 9, 0], 8, 2, 128, 16, fp8=fp8, W=13)
+    b["tables"] = torch.cat([b["tables"], torch.full((3, 200), -1, dtype=torch.int32)], 1)
+    ref, tol = TR.reference(b)
+    out = call(b, partition_size=part, max_query_len=400, max_ctx=b["tables"].shape[1] * 16)
+    assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("q", [2, 40])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [-0.09, 0.0])
+def test_scales_that_are_not_positive(q, fp8, scale):
+    b = TR.build(52, [150, 9], [q, q], 8, 2, 128, 16, fp8=fp8)
+    b["scale"] = scale
+    check(b)
+    check(b, softcap=3.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_workspace_of_any_size(fp8):
+    """The partitions are as many as the workspace holds."""
+    b = TR.build(53, [2500], [20], 8, 2, 128, 16, fp8=fp8)
+    ref, tol = TR.reference(b)
+    need = binding.paged_attention_tree_workspace_size(20, 8, 2, 128, 16, 20, 2520)
+    assert need > 0
+    for size in (need, need // 2, need // 3, 16):
+        out = call(b, workspace=torch.empty(size, dtype=torch.uint8, device=DEV))
+        assert R.worst(out, ref, tol) <= 1.0
+    assert binding.device_errors() == 0
+
+
+def test_a_large_tree():
+    """More nodes than a mask of paged_kv_tree_layout holds."""
+    b = TR.build(54, [17], [1100], 2, 1, 64, 16, "f16")
+    check(b)

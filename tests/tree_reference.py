@@ -73,7 +73,7 @@ def reference(b, softcap=0.0, key_begin=None):
             k, v = (x[blk, :, off].repeat_interleave(G, 1) for x in (kc, vc))  # [n][H][D]
             qt = b["q"][t].double()
             x = torch.einsum("hd,nhd->hn", qt, k) * b["scale"]
-            d = (D + 8) * 2.0 ** -23 * torch.einsum("hd,nhd->hn", qt.abs(), k.abs()) * b["scale"]
+            d = (D + 8) * 2.0 ** -23 * torch.einsum("hd,nhd->hn", qt.abs(), k.abs()) * abs(b["scale"])
             if softcap:
                 x = softcap * torch.tanh(x / softcap)
                 d = d + 1e-6 * x.abs()
