@@ -15,11 +15,11 @@
 // item after the other from the hardware's queue, the longest sequences first where the batch is small enough for the
 // order to be worked out in place (kTreeSortSeqs sequences).
 //
-// What bounds it: over a 16-bit pool HBM (19 sequences of 8192 tokens, 32/8 heads, trees of 32: 106 us, 6.07 TB/s, 89 %
+// What bounds it: over a 16-bit pool HBM (19 sequences of 8192 tokens, 32/8 heads, trees of 32: 102 us, 6.29 TB/s, 93 %
 // of the copy rate; a tile takes 0.75 us from HBM and 0.51 out of L2). An E4M3 tile, half the bytes, takes the same
 // 0.5 us: the S MMAs, whose N of 64 keys is short beside what it takes to bring in 128 rows of Q, hold their issuing
 // threads for 600 of a tile's 1000 cycles and the PV MMAs for 370, in turn for the two streams (tensor pipe 42 %, HBM
-// 48 %, issue slots 50 %). With a cap it is the rows' arithmetic, 1700 cycles a tile and stream (0.70 us). An item's
+// 48 %, issue slots 50 %). With a cap it is the rows' arithmetic, some 1600 cycles a tile and stream (0.65 us). An item's
 // start and end cost 2.6 us over a 16-bit pool and 5 over an E4M3 one. Two threads to a row, each with half of a tile's
 // keys, were slower (E4M3: 0.70 us a tile): what a tile costs a warp besides its keys doubles.
 //
@@ -60,7 +60,7 @@ struct TreeTcShape {
   static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
   static constexpr int OFF_ML = OFF_INFO + 2 * 64;                       // the streams' (m, l) at an item's end
   static constexpr int OFF_ORDER = OFF_ML + 4 * ROWS * 4;
-  static constexpr int OFF_EXPS = OFF_ORDER + kTreeSortSeqs;                      // FP8 pool, bf16 query: the rows' powers of two
+  static constexpr int OFF_EXPS = OFF_ORDER + kTreeSortSeqs;             // FP8 pool, bf16 query: the rows' powers of two
   static constexpr int SMEM = OFF_EXPS + (F8 ? ROWS : 0);
   static constexpr int S_COL = 0, O_COL = 256;  // tensor memory: stream w's S at 128 w, its O at 256 + 128 w
   static constexpr int TMEM_COLS = 512;
@@ -138,12 +138,13 @@ __device__ __forceinline__ TreeItem tree_item(const DecodeParams& p, const Score
 // FP8 pool: one warp widens a tile's 64 rows of 128 codes at src to f16 in the operand layout at slot. Lane (t = lane
 // / 8, c = lane % 8) takes codes 16 c .. 16 c + 15 of token 4 a + t as two groups of 8, which become two 16-byte
 // chunks of its row. Lanes take their second group first where c / 4 + t is odd, so that 16 lanes read all banks once
-// and 8 lanes store to all banks once: the f16 row's halves lie 1024 bytes apart.
+// and 8 lanes store to all banks once: the f16 row's halves lie 1024 bytes apart. (Two rounds of one loop: its code shares
+// the instruction caches with the rows', whose warps waited for instructions less. With a cap 121 us against 125.)
 __device__ __forceinline__ void tree_widen(unsigned char* slot, const unsigned char* src, int lane) {
   const int t = lane >> 3, c = lane & 7;
   const int g0 = ((c >> 2) + t) & 1;
   const unsigned char* from = src + t * 128 + 16 * c;
-#pragma unroll
+#pragma unroll 1
   for (int batch = 0; batch < 2; ++batch) {
     uint2 x[8][2];
 #pragma unroll
@@ -219,6 +220,17 @@ __device__ __forceinline__ void tree_fetch_q_bf16_as_f16(unsigned char* Qs, int 
         make_uint4(w[0], w[1], w[2], w[3]);
     if (c == 0) exps[r] = (signed char)k;
   }
+}
+
+// The largest magnitude of 64 values held as pairs.
+__device__ __forceinline__ float max64abs(const f32x2 (&x)[32]) {
+  float m[4], a, b;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    unpair2(x[u], a, b);
+    m[u & 3] = u < 4 ? fmaxf(fabsf(a), fabsf(b)) : max3(m[u & 3], fabsf(a), fabsf(b));
+  }
+  return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
 template <typename T, int D, int BS, bool F8, bool CAP>
@@ -690,23 +702,28 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         };
         const bool all_whole = __all_sync(kFull, whole);
         bool fast = false;  // the whole warp sees the whole tile, and the scores take their short form
-        float top = 0.f;
+        float big = 0.f;
         if (all_whole) {
           if constexpr (CAP) {
-            top = max64(x);
-            const float bottom = -max64neg(x);
-            fast = __all_sync(kFull, fmaxf(top, -bottom) <= near1);  // at most half the cap
-            if (cap_in < 0.f) top = bottom;
+            big = max64abs(x);
+            fast = __all_sync(kFull, big <= near1);  // at most half the cap
           } else {
             fast = sl2 >= 0.f;
           }
         }
         if (fast) {
           if constexpr (CAP) {
-            const f32x2 t1 = pair2(top, top), t2 = mul2(t1, t1);
-            float mx, unused;
-            unpair2(mul2(t1, fma2(t2, fma2(t2, fma2(t2, cc[3], cc[2]), cc[1]), cc[0])), mx, unused);
-            const float nm = reference(mx);
+            auto capped = [&](float v) {
+              const f32x2 t1 = pair2(v, v), t2 = mul2(t1, t1);
+              float mx, unused;
+              unpair2(mul2(t1, fma2(t2, fma2(t2, fma2(t2, cc[3], cc[2]), cc[1]), cc[0])), mx, unused);
+              return mx;
+            };
+            // (the largest magnitude bounds the scores: while no row's reference can move, their maximum is not needed.
+            // 117 us against 121)
+            float nm = -m_ref;
+            if (!__all_sync(kFull, fabsf(capped(big)) <= m_ref + 8.f))
+              nm = reference(capped(cap_in < 0.f ? -max64neg(x) : max64(x)));
             const f32x2 sub = pair2(nm, nm);
             lsum = weights64<TP>(scol + b * 64, [&](int u) {
               const f32x2 sq = mul2(x[u], x[u]);
@@ -719,7 +736,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           }
         } else {
           if constexpr (CAP) {
-            bool near = !all_whole && __all_sync(kFull, max3(max64(x), max64neg(x), 0.f) <= near1);
+            bool near = !all_whole && __all_sync(kFull, max64abs(x) <= near1);
             if (!near && !all_whole) {  // (a key that is not seen may hold anything)
               uint32_t see[2];
               seen(see);
