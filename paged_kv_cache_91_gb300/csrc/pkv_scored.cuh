@@ -119,6 +119,10 @@ __device__ __forceinline__ RowParts row_parts(int lo, int hi, int base, int P) {
   return {(lo - base) / P, (hi - 1 - base) / P};
 }
 
+// The SM's clock in steps of 2^kWorkClock, which a warp at long work stores as a sign of it for those that wait.
+constexpr int kWorkClock = 10;
+__device__ __forceinline__ int work_clock() { return (int)((unsigned long long)clock64() >> kWorkClock); }
+
 // This lane's D / 32 dims of a stored row (16-bit or E4M3 codes).
 template <int D, typename C>
 __device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned char* row, int lane) {
@@ -137,11 +141,11 @@ __device__ __forceinline__ void load_dims(float (&v)[D / 32], const unsigned cha
 // the lanes hold D / 32 dims each for their weighted values. The tiles multiply every key of a tile with every row,
 // a masked one with weight 0, and 0 times a NaN or infinite value is NaN: a row that such a value may have reached
 // is computed again here, where a masked key is not touched. pos: the row's position; TREE: that of node 0 (there is
-// no distance bias).
+// no distance bias). sign: where to leave a sign of work every 32 keys; or null.
 template <typename T, typename C, int D, bool TREE = false>
 __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams& sc, size_t row, int s, int h,
                                         int pos, int a, int b, int block_size, int lane, float& m, float& l,
-                                        float (&o)[D / 32]) {
+                                        float (&o)[D / 32], volatile int* sign = nullptr) {
   constexpr int DPL = D / 32, EB = CacheFmt<C>::EB, EPP = 16 / EB;
   const int g = h / p.group;
   const float slope = sc.slopes ? sc.slopes[h] * 1.4426950408889634f : 0.f;
@@ -151,6 +155,7 @@ __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams
   m = -INFINITY;
   l = 0.f;
   for (int j0 = a; j0 < b; j0 += 32) {
+    if (sign && lane == 0) *sign = work_clock();
     const int j = j0 + lane;
     const int phys = j < b ? p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size] : -1;
     bool ok = (unsigned)phys < (unsigned)p.num_blocks;  // (a bad id is reported by the tile)
@@ -202,15 +207,16 @@ __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams
 }
 
 // The first and the last key of [a, b) whose value row of kv head g holds a NaN or an infinity (first > last: none),
-// on one warp.
+// on one warp. sign as in scored_row, every 1024 keys.
 template <typename C, int D>
 __device__ __noinline__ void bad_values(const DecodeParams& p, int s, int g, int a, int b, int block_size, int lane,
-                                        int& first, int& last) {
+                                        int& first, int& last, volatile int* sign) {
   constexpr int EB = CacheFmt<C>::EB, CH = D * EB / 16, KPI = 32 / CH;  // pieces of a row, keys per load
   first = INT32_MAX;
   last = -1;
 #pragma unroll 4
   for (int j0 = a; j0 < b; j0 += KPI) {
+    if (((j0 - a) & 1023) == 0 && lane == 0) *sign = work_clock();
     const int j = j0 + lane / CH;
     if (j >= b) continue;
     const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];

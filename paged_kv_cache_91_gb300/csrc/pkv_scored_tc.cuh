@@ -31,7 +31,7 @@
 // Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 and 11 copy the
 // blocks of K and V tiles, half of each tile a warp (a copy takes about 100 cycles to issue), into a ring of
 // tile slots in the order K0 V0 K1 V1 ..., and 10 finds the items; FP8 pool: 12-15 widen a tile's codes to f16
-// in place. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop, set
+// in place. Every wait is bounded (work_wait): a copy or MMA that does not complete makes the CTA stop, set
 // PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has already claimed
 // for later stay as they were.
 #pragma once
@@ -113,7 +113,7 @@ struct ScoredTcShape {
   // pv_done; items: info_full[2], info_empty[2], next; q_shared
   static constexpr int NBARS = 24 + 16 + 6;
   static constexpr int OFF_NEXT = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;  // the hardware's answer: the next CTA
-  static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag
+  static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag, sign of work
   static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
   static constexpr int OFF_ML = OFF_INFO + 2 * 64;                       // stream 1's (m, l) in an item of shared rows
   static constexpr int SMEM = OFF_ML + 2 * ROWS * 4;
@@ -125,6 +125,35 @@ struct ScoredTcShape {
   static_assert(NBT >= 4 && NBT <= 16, "blocks per tile");
   static_assert(!F8 || D == 128, "an FP8 pool: head_dim 128");
 };
+
+// tc_wait for a warp that may have to wait while rows are computed again over a whole partition (10.8 us for 32 keys
+// of a row, up to 32 rows a warp: a second for 100,000 keys). Their warps leave a sign of work at abort[1] every few
+// microseconds, and the limit runs from the last one; what they do ends by itself. Such waits are those for an item,
+// its Q and its P, and for the place of an item or a tile to be free; a tile on its way and MMAs that were issued do
+// not wait for the rows, and the rows wait for tiles only when none of them is at such work (they meet at barriers
+// without a limit). OUT_OF_LINE: as a call, where instructions to fetch are what a kernel waits for (tree attention
+// over an E4M3 pool with a cap 117 us against 120; over a 16-bit pool 62 against 61, scored prompts 746 against
+// 724).
+__device__ __forceinline__ bool work_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const int t0 = work_clock();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const int now = work_clock();
+    if (min(now - t0, now - abort[1]) > (int)(kWaitLimitCycles >> kWorkClock)) {  // (a sign may be newer than now)
+      *abort = 1;
+      return false;
+    }
+  }
+}
+static __device__ __noinline__ bool work_wait_call(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return work_wait_on(bar, parity, abort);
+}
+template <bool OUT_OF_LINE>
+__device__ __forceinline__ bool work_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return OUT_OF_LINE ? work_wait_call(bar, parity, abort) : work_wait_on(bar, parity, abort);
+}
 
 // Whether every thread of the four widening warps says yes.
 __device__ __forceinline__ bool widen_agree(bool yes) {
@@ -459,7 +488,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     mbar_init(next_bar, 1);
     mbar_init(q_shared, ROWS);
     fence_mbar_init();
-    *abort = 0;
+    abort[0] = 0;
+    abort[1] = work_clock();
   }
   if (warp == Sh::MMA_WARP) tc::alloc(tmem_slot, Sh::TMEM_COLS);
   tc::fence_before_sync();
@@ -468,7 +498,9 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   const uint32_t tbase = *tmem_slot;
 
   // Item k, read by a whole warp; its place is then free again. False: none came in time.
-  auto wait_item = [&](int k) { return __all_sync(kFull, tc_wait(info_full + (k & 1), (k >> 1) & 1, abort)) != 0; };
+  auto wait_item = [&](int k) {
+    return __all_sync(kFull, work_wait<false>(info_full + (k & 1), (k >> 1) & 1, abort)) != 0;
+  };
   auto free_item = [&](int k) {
     __syncwarp();
     if (lane == 0) mbar_arrive(info_empty + (k & 1));
@@ -520,7 +552,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           m.ntile = -1;  // (nothing is asked again)
         have = false;
       }
-      if (ok && k >= 2) ok = __all_sync(kFull, tc_wait(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
+      if (ok && k >= 2) ok = __all_sync(kFull, work_wait<false>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (!ok) return;
       if (lane == 0) {
         *info(k) = m;
@@ -549,7 +581,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
           uint64_t* bar = landed + it % NS;
-          if (it >= NS) ok = __all_sync(kFull, tc_wait(empty + it % NS, (it / NS - 1) & 1, abort));
+          if (it >= NS) ok = __all_sync(kFull, work_wait<false>(empty + it % NS, (it / NS - 1) & 1, abort));
           if (!ok) break;
           if (lane == 0) {
             fence_proxy_async_smem();  // generic stores into the slot (zeroed rows, widened codes): before the copies
@@ -643,8 +675,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         auto pv_read = [&](int hf) { return cnt == 0 || tc_wait(pv_done + 2 * st + hf, (cnt - 1) & 1, abort); };
         // Shared rows are stream 0's to bring, so stream 1 waits for those too, on a barrier of shared items alone:
         // of q_full[0] it would leave out the other items' phases, and in those the streams may be an item apart.
-        ok = tc_wait(q_full + st, nq & 1, abort) &&
-             (st == 0 || !shared || tc_wait(q_shared, nshared++ & 1, abort));
+        ok = work_wait<false>(q_full + st, nq & 1, abort) &&
+             (st == 0 || !shared || work_wait<false>(q_shared, nshared++ & 1, abort));
         if (first > 0) ok = ok && skip_tile(0);
         if (first < m.ntile) {
           ok = ok && pv_read(0) && issue_s(first, 0) && pv_read(1) && issue_s(first, 1);
@@ -655,7 +687,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           }
           ++cnt;
           for (int hf = 0; ok && hf < 2; ++hf) {
-            ok = tc_wait(p_full + 2 * st + hf, (cnt - 1) & 1, abort);
+            ok = work_wait<false>(p_full + 2 * st + hf, (cnt - 1) & 1, abort);
             tc::commit(pv_done + 2 * st + hf);
           }
         }
@@ -665,7 +697,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           ++cnt;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            ok = ok && tc_wait(p_full + 2 * st + hf, (cnt - 1) & 1, abort) &&
+            ok = ok && work_wait<false>(p_full + 2 * st + hf, (cnt - 1) & 1, abort) &&
                  (hf > 0 || tc_wait(full + iv % NS, (iv / NS) & 1, abort));
             if (!ok) break;
             tc::fence_after_sync();
@@ -1084,7 +1116,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         uint32_t redo = __ballot_sync(kFull, mine && !fine && ok && l == l && (lo > m.c0 || hi < m.c1));
         if (redo) {
           int bad0, bad1;
-          bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1);
+          bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1, abort + 1);
           redo &= __ballot_sync(kFull, bad0 > bad1 || lo > bad0 || hi <= bad1);
         }
         for (; redo; redo &= redo - 1) {
@@ -1094,7 +1126,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           const int at = __shfl_sync(kFull, orow, src);
           const bool rdirect = __shfl_sync(kFull, (int)direct, src);
           float rm, rl, o[D / 32];
-          scored_row<T, C, D>(p, sc, at, m.s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o);
+          scored_row<T, C, D>(p, sc, at, m.s, rh, rpos, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o,
+                              abort + 1);
           store_row<T, D>(p, at, m.part, rdirect, lane, rm, rl, o);
         }
       }

@@ -25,9 +25,9 @@
 //
 // Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 copies K, 11 copies V and
 // finds the items; FP8 pool: 12-15 widen the codes of one (stream, K or V) ring each to f16, from the slots where they
-// land to the ring that the MMAs read. Every wait is bounded: a copy or MMA that does not complete makes the CTA stop,
-// set PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has already claimed
-// for later stay as they were.
+// land to the ring that the MMAs read. Every wait is bounded (work_wait): a copy or MMA that does not complete makes
+// the CTA stop, set PKV_DEVERR_TIMEOUT and write zeros for the rows of the item at hand. The rows of one that it has
+// already claimed for later stay as they were.
 #pragma once
 
 #include <type_traits>
@@ -56,7 +56,7 @@ struct TreeTcShape {
   // items: info_full[2], info_empty[2], next
   static constexpr int NBARS = 2 * NS + 8 * NC + 4 + 2 + 1 + 5;
   static constexpr int OFF_NEXT = (OFF_BARS + NBARS * 8 + 15) / 16 * 16;  // the hardware's answer: the next CTA
-  static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag
+  static constexpr int OFF_MISC = OFF_NEXT + 16;                         // tensor-memory base, abort flag, sign of work
   static constexpr int OFF_INFO = OFF_MISC + 16;                         // two items
   static constexpr int OFF_ML = OFF_INFO + 2 * 64;                       // the streams' (m, l) at an item's end
   static constexpr int OFF_ORDER = OFF_ML + 4 * ROWS * 4;
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     mbar_init(q_full, 2 * ROWS);
     mbar_init(next_bar, 1);
     fence_mbar_init();
-    *abort = 0;
+    abort[0] = 0;
+    abort[1] = work_clock();
   }
   if (warp == Sh::MMA_WARP) tc::alloc(tmem_slot, Sh::TMEM_COLS);
   tc::fence_before_sync();
@@ -311,7 +312,9 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
   }
 
   // Item k, read by a whole warp; its place is then free again. False: none came in time.
-  auto wait_item = [&](int k) { return __all_sync(kFull, tc_wait(info_full + (k & 1), (k >> 1) & 1, abort)) != 0; };
+  auto wait_item = [&](int k) {
+    return __all_sync(kFull, work_wait<F8>(info_full + (k & 1), (k >> 1) & 1, abort)) != 0;
+  };
   auto free_item = [&](int k) {
     __syncwarp();
     if (lane == 0) mbar_arrive(info_empty + (k & 1));
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       then.ntile = -1;
       if (have) then = tree_item<BS, NT>(p, sc, x, y, sc.sort_seqs ? order[z] : z, lane);
       if (then.ntile == -2) return false;
-      if (k >= 2) ok = __all_sync(kFull, tc_wait(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
+      if (k >= 2) ok = __all_sync(kFull, work_wait<F8>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (ok && lane == 0) {
         *info(k) = then;
         mbar_arrive(info_full + (k & 1));
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         const int n = __popc(__ballot_sync(kFull, mine));
         const int row = (id * p.num_kv_heads + m.kvh) * BS;  // first pool row of the block
         const int c = stream ? issued[1] : issued[0], i = (2 * stream + kv) * NL + c % NL;
-        if (c >= NL) ok = __all_sync(kFull, tc_wait((F8 ? codes_free : done) + i, (c / NL - 1) & 1, abort));
+        if (c >= NL) ok = __all_sync(kFull, work_wait<F8>((F8 ? codes_free : done) + i, (c / NL - 1) & 1, abort));
         if (!ok) break;
         if (lane == 0) {
           if (!F8) fence_proxy_async_smem();  // generic stores into the slot (zeroed rows): before the copies
@@ -462,8 +465,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         const int end = c + m.tiles(r >> 1);
         for (; ok && c < end; ++c) {
           const int from = r * NC + c % NC, to = slot_of(r >> 1, r & 1, c);
-          ok = __all_sync(kFull, tc_wait(raw + from, (c / NC) & 1, abort) &&
-                                     (c < NR || tc_wait(done + to, (c / NR - 1) & 1, abort)));
+          ok = __all_sync(kFull, work_wait<F8>(raw + from, (c / NC) & 1, abort) &&
+                                     (c < NR || work_wait<F8>(done + to, (c / NR - 1) & 1, abort)));
           if (!ok) break;
           tree_widen(slot(to), smem + Sh::OFF_CODES + from * Sh::CODES, lane);
           fence_proxy_async_smem();  // generic stores, read by the MMAs
@@ -512,12 +515,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           tc::commit(done + i);
           return true;
         };
-        ok = landed(0, cnt) && tc_wait(q_full, nq & 1, abort);
+        ok = landed(0, cnt) && work_wait<F8>(q_full, nq & 1, abort);
         for (int c = cnt; ok && c < min(end, cnt + 2); ++c) ok = landed(0, c) && issue_s(c);
         ok = ok && landed(1, cnt);
         for (int c = cnt; ok && c < end; ++c) {
           const int i = slot_of(st, 1, c);
-          ok = tc_wait(p_full + 2 * st + (c & 1), (c >> 1) & 1, abort);
+          ok = work_wait<F8>(p_full + 2 * st + (c & 1), (c >> 1) & 1, abort);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t b_desc = v_desc + (uint64_t)((c % NR) * (Sh::TILE / 16));
@@ -910,7 +913,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             kFull, mine && !fine && ok && l == l && (lo > m.c0 || hi < m.c1 || m.c1 > node0));
         if (redo) {
           int bad0, bad1;
-          bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1);
+          bad_values<C, D>(p, m.s, m.kvh, m.c0, m.c1, BS, lane, bad0, bad1, abort + 1);
           redo &= __ballot_sync(kFull, bad0 > bad1 || lo > bad0 || hi <= bad1 || bad1 >= node0);
         }
         for (; redo; redo &= redo - 1) {
@@ -919,7 +922,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           const int rh = __shfl_sync(kFull, h, src), at = __shfl_sync(kFull, orow, src);
           const bool rdirect = __shfl_sync(kFull, (int)direct, src);
           float rm, rl, o[D / 32];
-          scored_row<T, C, D, true>(p, sc, at, m.s, rh, node0, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o);
+          scored_row<T, C, D, true>(p, sc, at, m.s, rh, node0, max(rlo, tok0), min(rhi, tok0 + P), BS, lane, rm, rl, o,
+                                    abort + 1);
           if ((lane >> 4) == w) {  // (D / 32 dims a lane)
             constexpr int DPL = D / 32;
             if (rdirect) {
