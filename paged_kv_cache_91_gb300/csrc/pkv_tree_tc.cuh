@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       mbar_init(info_full + k, 1);
       mbar_init(info_empty + k, Sh::THREADS / 32 - 1);  // every warp but the one that finds the items
     }
-    mbar_init(q_full, 2 * ROWS);
+    mbar_init(q_full, 2 * ROWS + 2);  // and the threads that issue MMAs, once they have seen the Q before
     mbar_init(next_bar, 1);
     fence_mbar_init();
     abort[0] = 0;
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     TreeItem m;
     int cnt = 0, nq = 0;  // this stream's tiles and the items with keys before
     bool ok = true;
+    if (lane == 0) mbar_arrive(q_full);
     for (int k = 0; ok; ++k) {
       ok = read_item(k, m);
       if (!ok || m.ntile < 0) break;
@@ -515,7 +516,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
           tc::commit(done + i);
           return true;
         };
+        // (a stream without tiles in an item holds nobody up there: by its arrival the next Q's phase cannot complete
+        // before it has seen this one's, whose parity would be that of the one after next)
         ok = landed(0, cnt) && work_wait<F8>(q_full, nq & 1, abort);
+        if (ok) mbar_arrive(q_full);
         for (int c = cnt; ok && c < min(end, cnt + 2); ++c) ok = landed(0, c) && issue_s(c);
         ok = ok && landed(1, cnt);
         for (int c = cnt; ok && c < end; ++c) {
