@@ -847,8 +847,9 @@ pkv_status_t paged_kv_write_rope_fp8(void* query_out, const void* query, const v
  *                may be NULL when that size is 0
  *   *_fp8        over an E4M3 pool; head_dim 128 only
  *
- * Everything else (the other arguments and limits, precision, the error word,
- * rows that are not seen, blocks that no token of a sequence sees) is as in
+ * A table entry of drafted places that no token's mask names has no effect,
+ * whatever it holds. Everything else (the other arguments and limits, precision,
+ * the error word, rows and blocks that are not seen) is as in
  * paged_attention_multi_query_scored(_fp8), but for the last limit: with more
  * than 8 rows per kv head, num_seqs * num_kv_heads * partitions *
  * ceil(max_query_len * (num_heads / num_kv_heads) / 128) at most 2^27.

@@ -69,6 +69,11 @@ __device__ __forceinline__ int scored_query_len(const ScoreParams& sc, int s, in
   return q1 - q0;
 }
 
+// The n lowest bits (all from 32 on, none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // The visible keys [lo, hi) of query token t at position p in a context of ctx tokens (hi >= lo). TREE: the query
 // tokens are nodes of a tree, the context's last q_len positions; of those a token sees the ones in its mask, so that
 // its interval ends with the context.
@@ -95,6 +100,20 @@ __device__ __forceinline__ uint32_t tree_bits(const ScoreParams& sc, int t, int 
   const uint32_t a = w < 0 ? 0xffffffffu : w < sc.mask_words ? words[w] : 0u;
   const uint32_t b = w + 1 < sc.mask_words ? words[w + 1] : 0u;
   return __funnelshift_r(a, b, u & 31);
+}
+
+// TREE: whether one of the tokens ta .. tb of a sequence (its context ctx tokens, its first query row q0) sees a key of
+// the block that starts at place at. Asked only of a block with a bad id: an error if it is seen, else nothing.
+template <bool TREE, int BS>
+__device__ __noinline__ bool block_seen(const ScoreParams& sc, int q0, int q_len, int ctx, int ta, int tb, int at) {
+  for (int t = ta; t <= tb; ++t) {
+    int lo, hi;
+    scored_span<TREE>(sc, q0 + t, ctx - q_len + t, ctx, lo, hi);
+    uint32_t see = low_bits(min(hi - at, BS)) & ~low_bits(lo - at);
+    if (see) see &= tree_bits(sc, q0 + t, at - (ctx - q_len));
+    if (see) return true;
+  }
+  return false;
 }
 
 // A sequence's partitions: partition k holds the positions [base + k P, base + (k + 1) P), where base is the

@@ -169,11 +169,6 @@ __device__ __forceinline__ bool widen_agree(bool yes) {
   return r != 0;
 }
 
-// The n lowest bits (all from 32 on, none for n <= 0).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 // -inf for the keys 2 u, 2 u + 1 whose bits of see are not set.
 __device__ __forceinline__ void mask64(f32x2 (&x)[32], const uint32_t (&see)[2]) {
 #pragma unroll

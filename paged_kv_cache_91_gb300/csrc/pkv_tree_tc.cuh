@@ -398,7 +398,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       auto load_ids = [&](int b0) { return b0 + lane < nblk ? table[b0 + lane] : -1; };
       auto checked = [&](int b0, int id) {
         if (b0 + lane < nblk && (unsigned)id >= (unsigned)p.num_blocks) {
-          atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+          const int last = (int)((m.row0() + m.nrows(G) - 1) / G);
+          if (!finder && block_seen<true, BS>(sc, m.q0, m.q_len, m.ctx, (int)(m.row0() / G), last,
+                                              (blk0 + b0 + lane) * BS))
+            atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
           return -1;
         }
         return id;
