@@ -580,8 +580,8 @@ pkv_status_t paged_attention_decode_fp8(void* out, const void* query, const void
  *   *_fp8          over an E4M3 pool, k_scale and v_scale as in
  *                  paged_attention_decode_fp8; head_dim 128 only
  *
- * Block-table entries whose tokens no query token of the sequence sees are not
- * read, so that the blocks behind a window may have been given to others, and
+ * Block-table entries whose tokens no query token of the sequence sees have no
+ * effect, so that the blocks behind a window may have been given to others, and
  * K and V rows outside a query token's interval never enter its result,
  * whatever they hold. (Scores of other rows choose between forms of the tanh
  * that are equally exact, and a row next to a NaN or infinite value that it

@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t tree_bits(const ScoreParams& sc, int t, int 
   return __funnelshift_r(a, b, u & 31);
 }
 
-// TREE: whether one of the tokens ta .. tb of a sequence (its context ctx tokens, its first query row q0) sees a key of
+// Whether one of the tokens ta .. tb of a sequence (its context ctx tokens, its first query row q0) sees a key of
 // the block that starts at place at. Asked only of a block with a bad id: an error if it is seen, else nothing.
 template <bool TREE, int BS>
 __device__ __noinline__ bool block_seen(const ScoreParams& sc, int q0, int q_len, int ctx, int ta, int tb, int at) {
@@ -110,7 +110,9 @@ __device__ __noinline__ bool block_seen(const ScoreParams& sc, int q0, int q_len
     int lo, hi;
     scored_span<TREE>(sc, q0 + t, ctx - q_len + t, ctx, lo, hi);
     uint32_t see = low_bits(min(hi - at, BS)) & ~low_bits(lo - at);
-    if (see) see &= tree_bits(sc, q0 + t, at - (ctx - q_len));
+    if constexpr (TREE) {
+      if (see) see &= tree_bits(sc, q0 + t, at - (ctx - q_len));
+    }
     if (see) return true;
   }
   return false;

@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(NW * 32, Tile::MIN_CTAS)
     const int v = p.block_tables[(size_t)s * p.max_blocks_per_seq + blk0 + warp + NW * lane];
     if ((unsigned)v < (unsigned)p.num_blocks) {
       my_phys = v;
-    } else if (!TREE || block_seen<true, BS>(sc, q0, q_len, ctx, row0 / G, (row0 + ncol - 1) / G,
-                                             (blk0 + warp + NW * lane) * BS)) {
+    } else if (block_seen<TREE, BS>(sc, q0, q_len, ctx, row0 / G, (row0 + ncol - 1) / G,
+                                    (blk0 + warp + NW * lane) * BS)) {
       atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
     }
   }

@@ -568,7 +568,9 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         int id = next;
         if (j + 1 < m.ntile) next = load_id(j + 1);
         if (lane < NH && j * NBT + at < nblk && (unsigned)id >= (unsigned)p.num_blocks) {
-          atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
+          const int last = (int)((m.row0() + m.nrows(G) - 1) / G);
+          if (block_seen<false, BS>(sc, m.q0, m.q_len, m.ctx, (int)(m.row0() / G), last, (blk0 + j * NBT + at) * BS))
+            atomicOr(p.err, PKV_DEVERR_BLOCK_ID);
           id = -1;
         }
         const int n = __popc(__ballot_sync(kFull, id >= 0));
