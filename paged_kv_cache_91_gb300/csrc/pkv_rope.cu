@@ -54,6 +54,11 @@ struct Part {
 __device__ __forceinline__ Part load_part(const unsigned char* row, int da, int db) {
   return {__ldg(reinterpret_cast<const uint2*>(row + da * 2)), __ldg(reinterpret_cast<const uint2*>(row + db * 2))};
 }
+// The same of a query row, which the call may write in place: not through the read-only path, which holds only what a
+// kernel does not write.
+__device__ __forceinline__ Part load_query(const unsigned char* row, int da, int db) {
+  return {*reinterpret_cast<const uint2*>(row + da * 2), *reinterpret_cast<const uint2*>(row + db * 2)};
+}
 __device__ __forceinline__ void store_part(unsigned char* row, int da, int db, const Part& y) {
   *reinterpret_cast<uint2*>(row + da * 2) = y.a;
   *reinterpret_cast<uint2*>(row + db * 2) = y.b;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pkv_write_rope_kernel
   Part q_in[kRopeUnroll], k_in, v_in;
 #pragma unroll
   for (int u = 0; u < kRopeUnroll; ++u)
-    if (first + g + u * step < H) q_in[u] = load_part(q + (size_t)u * step * D * 2, da, db);
+    if (first + g + u * step < H) q_in[u] = load_query(q + (size_t)u * step * D * 2, da, db);
   if (first + g < Hkv) {
     k_in = load_part(k, da, db);
     v_in = load_part(v, da, db);
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pkv_write_rope_kernel
       if (base + u * step >= H) break;
       const int r = base + u * step + g;
       const Part y = q_in[u];
-      if (r + kRopeUnroll * step < H) q_in[u] = load_part(q + (size_t)(kRopeUnroll + u) * step * D * 2, da, db);
+      if (r + kRopeUnroll * step < H) q_in[u] = load_query(q + (size_t)(kRopeUnroll + u) * step * D * 2, da, db);
       f32x2 x[4];
       norm_and_turn<T, D, INTERLEAVED>(y, turn, p.eps, x);
       Part z = {make_uint2(pack2<T>(x[0]), pack2<T>(x[1])), make_uint2(pack2<T>(x[2]), pack2<T>(x[3]))};
