@@ -309,7 +309,7 @@ pkv_status_t scored_impl(const ScoredCall& c, bool decode) {
   if ((long long)pl.np * pl.row_tiles >= (1LL << 31))
     return fail(PKV_ERR_UNSUPPORTED, "partitions * row tiles must be < 2^31");
   // A CTA of the tensor tile looks through the grid for rows, some 0.6 us an empty place (measured: 65536 places for 64
-  // sequences of one token, 257 us on 152 SMs), and whoever waits for its next rows waits a second at most.
+  // sequences of one token, 257 us on 152 SMs): the limit keeps a call without work to half a second.
   if (pl.tensor && (long long)pl.np * pl.row_tiles * c.num_kv_heads * c.num_seqs > kScoredMaxItems)
     return fail(PKV_ERR_UNSUPPORTED,
                 "num_seqs * num_kv_heads * partitions (%d) * row tiles (%d, of max_query_len) must be <= 2^27", pl.np,

@@ -127,13 +127,14 @@ struct ScoredTcShape {
 };
 
 // tc_wait for a warp that may have to wait while rows are computed again over a whole partition (10.8 us for 32 keys
-// of a row, up to 32 rows a warp: a second for 100,000 keys). Their warps leave a sign of work at abort[1] every few
-// microseconds, and the limit runs from the last one; what they do ends by itself. Such waits are those for an item,
-// its Q and its P, and for the place of an item or a tile to be free; a tile on its way and MMAs that were issued do
-// not wait for the rows, and the rows wait for tiles only when none of them is at such work (they meet at barriers
-// without a limit). OUT_OF_LINE: as a call, where instructions to fetch are what a kernel waits for (tree attention
-// over an E4M3 pool with a cap 117 us against 120; over a 16-bit pool 62 against 61, scored prompts 746 against
-// 724).
+// of a row, up to 32 rows a warp: a second for 100,000 keys), or while a place of the grid that holds work is looked
+// for (0.6 us an empty place; 2^27 of them are half a second if all SMs look). The warps that are at it leave a sign
+// of work at abort[1] every few microseconds, and the limit runs from the last one; what they do ends by itself.
+// Such waits are those for an item, its Q and its P, and for the place of an item or a tile to be free; a tile on
+// its way and MMAs that were issued do not wait for the rows, and the rows wait for tiles only when none of them is
+// at such work (they meet at barriers without a limit). OUT_OF_LINE: as a call, where instructions to fetch are what
+// a kernel waits for (tree attention over an E4M3 pool with a cap 117 us against 120; over a 16-bit pool 62 against
+// 61, scored prompts 746 against 724).
 __device__ __forceinline__ bool work_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const int t0 = work_clock();
   for (;;) {
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         else
           m.ntile = -1;  // (nothing is asked again)
         have = false;
+        if (lane == 0) abort[1] = work_clock();
       }
       if (ok && k >= 2) ok = __all_sync(kFull, work_wait<false>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (!ok) return;

@@ -353,7 +353,10 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     auto publish = [&](int k, bool have, int x, int y, int z) {
       then.ntile = -1;
       if (have) then = tree_item<BS, NT>(p, sc, x, y, sc.sort_seqs ? order[z] : z, lane);
-      if (then.ntile == -2) return false;
+      if (then.ntile == -2) {
+        if (lane == 0) abort[1] = work_clock();
+        return false;
+      }
       if (k >= 2) ok = __all_sync(kFull, work_wait<F8>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (ok && lane == 0) {
         *info(k) = then;

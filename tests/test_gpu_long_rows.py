@@ -112,3 +112,44 @@ def test_scored():
             workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
 
     check(b, [set(range(i + 1)) for i in range(Q)], bad, call)
+
+
+@pytest.mark.parametrize("scored", [False, True])
+def test_a_grid_of_empty_places_beside_another_call(scored):
+    """The largest grid that a call accepts, nearly all of it empty, on the third of the SMs that another call leaves for
+    more than a second."""
+    b, sets = batch(False, 2), [{0, i} for i in range(Q)]
+    seqs = 13  # 104 CTAs of the long rows
+    mask = i32([[sum(1 << u for u in x)] for x in sets] * seqs)
+    q = b["q"].repeat(seqs, 1, 1).to(DEV)
+    k, v = b["k"].to(DEV), b["v"].to(DEV)
+    tables = torch.stack([b["tables"][0]] * seqs).to(torch.int32).to(DEV)
+    busy, out = torch.full_like(q, 7.0), torch.full((48, 8, D), 7.0, dtype=q.dtype, device=DEV)
+    n, ql, blocks = 65535, 48, 256  # sequences (the last one has all tokens), their tokens, partitions of a block each
+    few = torch.zeros((n, blocks), dtype=torch.int32, device=DEV)
+    few[-1] = torch.arange(blocks, device=DEV) % 50
+    ctx, starts = i32([0] * n), i32([0] * (n + 1))
+    ctx[-1], starts[-1] = blocks * B, ql
+    few_q = torch.randn((ql, 8, D), generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    lens = (i32([LONG] * seqs), i32([Q * s for s in range(seqs + 1)]))
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    full = i32([[-1, -1]] * ql)
+    kw = dict(max_query_len=ql, max_context_len=blocks * B, partition_size=B)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    binding.paged_attention_tree(busy, q, k, v, tables, *lens, mask, D ** -0.5, max_query_len=Q, max_context_len=LONG,
+                                 workspace=small, stream=streams[0])
+    if scored:
+        binding.paged_attention_multi_query_scored(out, few_q, k, v, few, ctx, starts, D ** -0.5, stream=streams[1],
+                                                   key_end=i32([blocks * B] * ql), **kw)
+    else:
+        binding.paged_attention_tree(out, few_q, k, v, few, ctx, starts, full, D ** -0.5, stream=streams[1], **kw)
+    torch.cuda.synchronize()
+    assert binding.device_errors() == 0
+    want = torch.empty_like(out)
+    args = (want, few_q, k, v, few[-1:], ctx[-1:], i32([0, ql]))
+    if scored:
+        binding.paged_attention_multi_query_scored(*args, D ** -0.5, key_end=i32([blocks * B] * ql), **kw)
+    else:
+        binding.paged_attention_tree(*args, full, D ** -0.5, **kw)
+    assert torch.isfinite(out).all() and torch.equal(out, want)
