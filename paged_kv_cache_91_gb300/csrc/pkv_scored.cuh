@@ -142,7 +142,7 @@ __device__ __forceinline__ RowParts row_parts(int lo, int hi, int base, int P) {
 
 // The SM's clock in steps of 2^kWorkClock, which a warp at long work stores as a sign of it for those that wait.
 constexpr int kWorkClock = 10;
-__device__ __forceinline__ int work_clock() { return (int)((unsigned long long)clock64() >> kWorkClock); }
+__device__ __forceinline__ unsigned work_clock() { return (unsigned)((unsigned long long)clock64() >> kWorkClock); }
 
 // This lane's D / 32 dims of a stored row (16-bit or E4M3 codes).
 template <int D, typename C>
@@ -176,7 +176,7 @@ __device__ __noinline__ void scored_row(const DecodeParams& p, const ScoreParams
   m = -INFINITY;
   l = 0.f;
   for (int j0 = a; j0 < b; j0 += 32) {
-    if (sign && lane == 0) *sign = work_clock();
+    if (sign && lane == 0) *sign = (int)work_clock();
     const int j = j0 + lane;
     const int phys = j < b ? p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size] : -1;
     bool ok = (unsigned)phys < (unsigned)p.num_blocks;  // (a bad id is reported by the tile)
@@ -237,7 +237,7 @@ __device__ __noinline__ void bad_values(const DecodeParams& p, int s, int g, int
   last = -1;
 #pragma unroll 4
   for (int j0 = a; j0 < b; j0 += KPI) {
-    if (((j0 - a) & 1023) == 0 && lane == 0) *sign = work_clock();
+    if (((j0 - a) & 1023) == 0 && lane == 0) *sign = (int)work_clock();
     const int j = j0 + lane / CH;
     if (j >= b) continue;
     const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / block_size];

@@ -136,12 +136,12 @@ struct ScoredTcShape {
 // a kernel waits for (tree attention over an E4M3 pool with a cap 117 us against 120; over a 16-bit pool 62 against
 // 61, scored prompts 746 against 724).
 __device__ __forceinline__ bool work_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const int t0 = work_clock();
+  const unsigned t0 = work_clock();
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    const int now = work_clock();
-    if (min(now - t0, now - abort[1]) > (int)(kWaitLimitCycles >> kWorkClock)) {  // (a sign may be newer than now)
+    const unsigned now = work_clock();  // (a sign may be newer)
+    if (min((int)(now - t0), (int)(now - (unsigned)abort[1])) > (int)(kWaitLimitCycles >> kWorkClock)) {
       *abort = 1;
       return false;
     }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     mbar_init(q_shared, ROWS);
     fence_mbar_init();
     abort[0] = 0;
-    abort[1] = work_clock();
+    abort[1] = (int)work_clock();
   }
   if (warp == Sh::MMA_WARP) tc::alloc(tmem_slot, Sh::TMEM_COLS);
   tc::fence_before_sync();
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         else
           m.ntile = -1;  // (nothing is asked again)
         have = false;
-        if (lane == 0) abort[1] = work_clock();
+        if (lane == 0) abort[1] = (int)work_clock();
       }
       if (ok && k >= 2) ok = __all_sync(kFull, work_wait<false>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (!ok) return;

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     mbar_init(next_bar, 1);
     fence_mbar_init();
     abort[0] = 0;
-    abort[1] = work_clock();
+    abort[1] = (int)work_clock();
   }
   if (warp == Sh::MMA_WARP) tc::alloc(tmem_slot, Sh::TMEM_COLS);
   tc::fence_before_sync();
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
       then.ntile = -1;
       if (have) then = tree_item<BS, NT>(p, sc, x, y, sc.sort_seqs ? order[z] : z, lane);
       if (then.ntile == -2) {
-        if (lane == 0) abort[1] = work_clock();
+        if (lane == 0) abort[1] = (int)work_clock();
         return false;
       }
       if (k >= 2) ok = __all_sync(kFull, work_wait<F8>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
