@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         else
           m.ntile = -1;  // (nothing is asked again)
         have = false;
-        if (lane == 0) abort[1] = (int)work_clock();
+        if (m.ntile == -2 && lane == 0) abort[1] = (int)work_clock();
       }
       if (ok && k >= 2) ok = __all_sync(kFull, work_wait<false>(info_empty + (k & 1), ((k >> 1) - 1) & 1, abort));
       if (!ok) return;
