@@ -976,7 +976,8 @@ def paged_attention_tree(out: torch.Tensor, query: torch.Tensor, key_cache: torc
     are its last q_len context positions, and each sees the committed positions before them and the drafted ones whose
     bits are set in its tree_mask row ([T][words] int32, see paged_kv_tree_layout). ``softcap`` as in
     paged_attention_decode_scored; ``key_begin`` [T] int32: a first visible key per token (a window, or 2**31 - 1 for
-    the tokens of a sequence that waits).
+    the tokens of a sequence that waits). It counts places in the cache, not positions: a window that is not longer than
+    the tree is deep also has to leave the ancestors behind it out of tree_mask.
 
     ``max_query_len`` bounds every tree on the host; when omitted it is read from query_start_loc, which synchronises
     the call's stream.

@@ -9,7 +9,9 @@
 // dims in a row.
 //
 // Bound by HBM once the batch is large, with the issue slots close behind (16384 tokens, 32/8 heads, bf16: 72 us, 5.7 TB/s,
-// 84 % of the copy rate; issue 73 %); a step's 256 tokens into an E4M3 pool take 4.7 us replayed from a graph, latency.
+// 84 % of the copy rate; issue 73 %; into an E4M3 pool, whose rows are divided and converted too, 80 us of 56); a step's
+// 256 tokens into an E4M3 pool take 4.7 us replayed from a graph, latency. At 64 registers a thread all but one of the
+// forms spill: 52 bytes stored and 76 loaded in the bf16 one above, up to 84 and 168 for f16 rows into an E4M3 pool.
 // On the way there (16384 tokens, with the launch, us): eight dims in a row a lane with the partner's values by shuffle 122,
 // pairs within a lane 107, 64 registers a thread for 8 CTAs an SM 98, packed arithmetic and loops of their own for
 // queries, keys and values 88.

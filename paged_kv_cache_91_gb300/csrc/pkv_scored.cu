@@ -171,16 +171,17 @@ ScoredPlan scored_plan(bool fp8, int num_query_tokens, int num_heads, int num_kv
 }
 
 // Tree attention: the tensor-memory tile (128 rows a CTA) from the second 8-column tile on. Measured, us a call, 8-column
-// and tensor tile, 64 contexts of 1000 to 3000 tokens, 32/8 heads: 16-bit pool 8 rows 110, 109; 12 rows 119, 107; 16 rows
-// 126, 111; 32 rows 210, 113; head_dim 64: 8 rows 67, 72; 12 rows 97, 76; E4M3: 8 rows 72, 97; 12 rows 106, 97; 32 rows
-// 199, 101; 4 contexts of 9001 to 32768, 40 heads: 8 rows 298, 352; 24 rows 407, 307.
+// and tensor tile, 64 contexts of 1000 to 3000 tokens, 32/8 heads: 16-bit pool 8 rows 93, 95; 12 rows 109, 93; 16 rows
+// 115, 96; head_dim 64: 8 rows 56, 69; 12 rows 91, 73; E4M3: 8 rows 62, 88; 12 rows 101, 88; 32 rows 195, 92; 4 contexts
+// of 9001 to 32768, 40 heads: 8 rows 295, 304; 24 rows 537, 385.
 constexpr int kTreeTensorRows = 9, kTreeRowTile = 128;
 constexpr int kTreeSms = 152;
 // What a call takes in n equal partitions a sequence, us, if every context is of max_context_len: rounds of CTAs, each a
 // partition's 64-token tiles and an item's start and end, then the partials' way through memory and the reduce kernel.
-// (Measured per tile and item: 16-bit 0.75 and 3, E4M3 0.51 and 6; head_dim 64 about half a tile.) One long context of
-// 32768 tokens, 32/8 heads: 12 to 19 partitions 45, 6 60, 3 103; 4 contexts of 16384, 40 heads: 1 336, 4 248, 6 244, 12
-// 257; 64 contexts to 2048, 32/8 heads: 1 76, 2 105.
+// (Measured per tile and item: 16-bit 0.75 and 3, E4M3 0.51 and 6; head_dim 64 about half a tile. A cap, which costs an
+// E4M3 tile another 0.15, shorter contexts than the longest and their order are not in it.) One long context of 32768
+// tokens, 32/8 heads: 12 to 19 partitions 35 to 37, 10 38, 8 42; 4 contexts of 16384, 40 heads: 4 220, 6 217, 12 229; 64
+// contexts to 2048, 32/8 heads: 1 62, 2 90.
 float tree_cost(bool fp8, int head_dim, long long items, long long rows, long long span, long long n) {
   const float tile = head_dim == 64 ? 0.4f : fp8 ? 0.51f : 0.75f, item = fp8 ? 6.f : 3.f;
   const long long tiles = (span + n * 64 - 1) / (n * 64), rounds = (items * n + kTreeSms - 1) / kTreeSms;

@@ -39,8 +39,9 @@ constexpr int kLayoutNodes = 32;  // per CTA
 constexpr int kMaxTree = 1024;
 
 // A CTA takes kLayoutNodes nodes of a tree, a warp one at a time: it walks up to the root through the parents in
-// shared memory, and lane w keeps the mask's word w. Latency: 8 trees of up to 16 nodes 1.8 us replayed from a graph, 512
-// of up to 64 6.4 us.
+// shared memory, and lane w keeps the mask's word w. Latency: 8 trees of up to 16 nodes 1.8 us replayed from a graph; 512
+// of up to 64 6.4 us and a chain of 64 nodes 7.3, since a warp takes four nodes one after the other and every ancestor is a
+// load that waits for the one before (a chain of 1024 nodes 108 us, 64 of them 500).
 __global__ void __launch_bounds__(kLayoutWarps * 32) pkv_tree_layout_kernel(const LayoutParams p) {
   pdl_begin();
   __shared__ int16_t up[kMaxTree];

@@ -15,13 +15,17 @@
 // item after the other from the hardware's queue, the longest sequences first where the batch is small enough for the
 // order to be worked out in place (kTreeSortSeqs sequences).
 //
-// What bounds it: over a 16-bit pool HBM (19 sequences of 8192 tokens, 32/8 heads, trees of 32: 102 us, 6.29 TB/s, 93 %
-// of the copy rate; a tile takes 0.75 us from HBM and 0.51 out of L2). An E4M3 tile, half the bytes, takes the same
-// 0.5 us: the S MMAs, whose N of 64 keys is short beside what it takes to bring in 128 rows of Q, hold their issuing
-// threads for 600 of a tile's 1000 cycles and the PV MMAs for 370, in turn for the two streams (tensor pipe 42 %, HBM
-// 48 %, issue slots 50 %). With a cap it is the rows' arithmetic, some 1600 cycles a tile and stream (0.65 us). An item's
-// start and end cost 2.6 us over a 16-bit pool and 5 over an E4M3 one. Two threads to a row, each with half of a tile's
-// keys, were slower (E4M3: 0.70 us a tile): what a tile costs a warp besides its keys doubles.
+// What bounds it: over a 16-bit pool HBM (19 sequences of 8192 tokens, 32/8 heads, trees of 32: 101 to 105 us, 6.1 to
+// 6.4 TB/s, 91 to 94 % of the copy rate; a tile takes 0.75 us from HBM and 0.51 out of L2). An E4M3 tile, half the bytes,
+// takes the same 0.5 us: a stream has some 2000 cycles for each of its tiles, in which the S MMAs, whose N of 64 keys is
+// short beside what it takes to bring in 128 rows of Q, hold their issuing thread for 720 and the PV MMAs for 465, in turn
+// with the other stream's (tensor pipe 41 %, HBM 47 %, issue slots 50 %). Q in tensor memory, in place of one of the four
+// S buffers or of one O, would relieve them and is not built. With a cap it is the rows' arithmetic, some 1700 of a
+// stream's 2650 cycles a tile (0.65 us); the four warps' chains wait for S, load it and store P for another 460, with two
+// row warps a scheduler (issue slots 51 %). There the kernel's 128 registers do not hold everything: 20 to 28 bytes a
+// thread are spilled and 40 to 44 loaded. An item's start and end cost 2.6 us over a 16-bit pool and 5 over an E4M3 one.
+// Two threads to a row, each with half of a tile's keys, were slower (E4M3: 0.70 us a tile): what a tile costs a warp
+// besides its keys doubles. With more than 128 rows per kv head K and V come once a row tile.
 //
 // Warps: 0-3 and 4-7 the streams' rows; 8 and 9 issue a stream's MMAs (one thread each); 10 copies K, 11 copies V and
 // finds the items; FP8 pool: 12-15 widen the codes of one (stream, K or V) ring each to f16, from the slots where they
